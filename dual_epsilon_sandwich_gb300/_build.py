@@ -1,6 +1,6 @@
 """Build libmrn.so in-tree with nvcc for sm_103a (GB300).
 
-One translation unit per operation plus the C-ABI layer, compiled in parallel,
+One translation unit per operation plus the C-ABI layers, compiled in parallel,
 then linked into ``dual_epsilon_sandwich_gb300/libmrn.so`` (the CUDA runtime is
 linked statically).  No fast-math: sqrt and division stay IEEE-rounded.
 """
@@ -23,7 +23,8 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", 
          "-I", INCLUDE, "-I", CSRC]
 SOURCES = ["mrn_api.cpp", "mrn_ops_rmsnorm.cu", "mrn_ops_then_add.cu", "mrn_ops_sandwich.cu",
            "mrn_ops_add_rmsnorm.cu", "mrn_ops_then_add_scale.cu", "mrn_ops_rmsnorm_q8_1.cu",
-           "mrn_ops_seam_f16.cu", "mrn_ops_seam_bf16.cu", "mrn_seam_scale.cu"]
+           "mrn_ops_seam_f16.cu", "mrn_ops_seam_bf16.cu", "mrn_seam_scale.cu",
+           "mrn_train_api.cpp", "mrn_layernorm.cu", "mrn_norm_backward.cu", "mrn_dropout.cu"]
 
 
 def nvcc() -> str:

@@ -20,6 +20,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "mrn_checks.h"
 #include "mrn_internal.h"
 
 namespace {
@@ -37,7 +38,9 @@ constexpr int kMaxDevices = 64;
 std::atomic<int> g_sm_count[kMaxDevices];
 constexpr int kDefaultSmCount = 152;   // GB300
 
-int elem_bytes(mrn_dtype dt) { return dt == MRN_F32 ? 4 : 2; }
+}  // namespace
+
+namespace mrn {
 
 int sm_count_of_current_device() {
     int dev = 0;
@@ -58,6 +61,24 @@ int sm_count_of_current_device() {
     if (dev >= 0 && dev < kMaxDevices) g_sm_count[dev].store(count, std::memory_order_relaxed);
     return count;
 }
+
+bool launch_pdl() { return (t_launch_options & MRN_LAUNCH_PDL) != 0; }
+
+mrn_status launch_result(cudaError_t err, uint64_t launched) {
+    g_launch_count.fetch_add(launched, std::memory_order_relaxed);
+    if (err != cudaSuccess) {
+        t_last_cuda_error = static_cast<int>(err);
+        (void)cudaGetLastError();   // clear the non-sticky launch error
+        return MRN_ERR_CUDA;
+    }
+    return MRN_OK;
+}
+
+}  // namespace mrn
+
+namespace {
+
+using namespace mrn;   // the checks of mrn_checks.h and the functions above
 
 int64_t pow2_ceil(int64_t v) {
     int64_t p = 1;
@@ -547,34 +568,6 @@ bool resolve_forced(Geometry g, mrn::Op op, int64_t n, mrn_dtype dt, bool aligne
     return true;
 }
 
-struct Span {
-    uintptr_t lo;
-    uintptr_t hi;
-};
-
-Span span_of(const void *p, int64_t bytes) {
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return Span{lo, lo + static_cast<uintptr_t>(bytes)};
-}
-
-bool overlaps(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi; }
-
-// An output may coincide exactly with a row input or be disjoint from it.
-bool output_vs_row_input_ok(Span out, Span in) { return !overlaps(out, in) || out.lo == in.lo; }
-
-mrn_status check_common(int64_t rows, int64_t n, mrn_dtype dt, float eps1, float eps2) {
-    if (dt != MRN_F32 && dt != MRN_BF16) return MRN_ERR_UNSUPPORTED_DTYPE;
-    if (n < 1 || rows < 0) return MRN_ERR_INVALID_SIZE;
-    const int64_t e = elem_bytes(dt);
-    if (n > INT64_MAX / e) return MRN_ERR_INVALID_SIZE;
-    if (rows > 0 && rows > INT64_MAX / (n * e)) return MRN_ERR_INVALID_SIZE;
-    if (!(eps1 > 0.0f) || !std::isfinite(eps1)) return MRN_ERR_INVALID_EPS;
-    if (!(eps2 > 0.0f) || !std::isfinite(eps2)) return MRN_ERR_INVALID_EPS;
-    return MRN_OK;
-}
-
-bool aligned_to(const void *p, int64_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-
 // True when every given pointer sits at the same offset within 16 bytes (then
 // every row of the call starts at one offset in all its row operands).
 bool same_offset16(std::initializer_list<const void *> ptrs) {
@@ -629,13 +622,7 @@ mrn_status launch(const Call &c, bool aligned16, cudaStream_t stream) {
                   : mrn::launch_seam_f16(c.op, bf16, g, a, c.rows, stream, &launched);
         break;
     }
-    g_launch_count.fetch_add(launched, std::memory_order_relaxed);
-    if (err != cudaSuccess) {
-        t_last_cuda_error = static_cast<int>(err);
-        (void)cudaGetLastError();   // clear the non-sticky launch error
-        return MRN_ERR_CUDA;
-    }
-    return MRN_OK;
+    return launch_result(err, launched);
 }
 
 // The seam norms: the fused form (weighted) and the split route's weightless
@@ -873,21 +860,15 @@ mrn_status mrn_seam_scale(const void *u, const void *gamma, void *y, int64_t row
     const cudaError_t err = mrn::launch_seam_scale(
         seam == MRN_BF16, u, gamma, y, rows, n, a16 ? 8 : 1, sm_count_of_current_device(),
         (t_launch_options & MRN_LAUNCH_PDL) != 0, stream, &launched);
-    g_launch_count.fetch_add(launched, std::memory_order_relaxed);
-    if (err != cudaSuccess) {
-        t_last_cuda_error = static_cast<int>(err);
-        (void)cudaGetLastError();
-        return MRN_ERR_CUDA;
-    }
-    return MRN_OK;
+    return launch_result(err, launched);
 }
 
 const char *mrn_status_string(mrn_status status) {
     switch (status) {
     case MRN_OK: return "ok";
     case MRN_ERR_NULL_POINTER: return "a required pointer is NULL";
-    case MRN_ERR_INVALID_SIZE: return "invalid size (n < 1, rows < 0 or byte size overflow)";
-    case MRN_ERR_INVALID_EPS: return "eps must be finite and > 0";
+    case MRN_ERR_INVALID_SIZE: return "invalid size (n < 1, rows < 0, byte size overflow or workspace too small)";
+    case MRN_ERR_INVALID_EPS: return "eps must be finite and > 0 (a dropout probability 0 .. 1)";
     case MRN_ERR_UNSUPPORTED_DTYPE: return "unsupported dtype";
     case MRN_ERR_ALIASING: return "forbidden overlap between buffers";
     case MRN_ERR_MISALIGNED: return "pointer not aligned to its element size";

@@ -62,7 +62,9 @@ EXPORTS = ("mrn_rmsnorm", "mrn_rmsnorm_then_add", "mrn_norm_residual_norm",
            "mrn_status_string", "mrn_last_cuda_error", "mrn_query_geometry",
            "mrn_force_geometry", "mrn_launch_count", "mrn_wait_timeouts",
            "mrn_set_launch_options", "mrn_launch_options", "mrn_rmsnorm_seam",
-           "mrn_rmsnorm_unweighted", "mrn_seam_scale")
+           "mrn_rmsnorm_unweighted", "mrn_seam_scale", "mrn_layernorm", "mrn_dropout_add",
+           "mrn_dropout_add_layernorm", "mrn_norm_backward_workspace", "mrn_layernorm_backward",
+           "mrn_dropout_add_layernorm_backward", "mrn_rmsnorm_backward")
 
 
 class MrnError(RuntimeError):
@@ -91,7 +93,9 @@ _lib = None
 
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
+_u64 = ctypes.c_uint64
 _f = ctypes.c_float
+_d = ctypes.c_double
 _i = ctypes.c_int
 
 
@@ -118,9 +122,20 @@ def lib() -> ctypes.CDLL:
             L.mrn_rmsnorm_seam.argtypes = [_vp, _vp, _vp, _i64, _i64, _f, _i, _i, _vp]
             L.mrn_rmsnorm_unweighted.argtypes = [_vp, _vp, _i64, _i64, _f, _i, _i, _vp]
             L.mrn_seam_scale.argtypes = [_vp, _vp, _vp, _i64, _i64, _i, _vp]
+            L.mrn_layernorm.argtypes = [_vp] * 6 + [_i64, _i64, _f, _i, _vp]
+            L.mrn_dropout_add.argtypes = [_vp] * 4 + [_u64, _d, _i64, _i64, _i, _vp]
+            L.mrn_dropout_add_layernorm.argtypes = [_vp] * 9 + [_u64, _d, _i64, _i64, _f, _i, _vp]
+            L.mrn_norm_backward_workspace.argtypes = [_i64, _i64, ctypes.POINTER(_i64)]
+            L.mrn_layernorm_backward.argtypes = [_vp] * 10 + [_i64, _i64, _i64, _i, _vp]
+            L.mrn_dropout_add_layernorm_backward.argtypes = \
+                [_vp] * 11 + [_u64, _d, _vp, _i64, _i64, _i64, _i, _vp]
+            L.mrn_rmsnorm_backward.argtypes = [_vp] * 7 + [_i64, _i64, _i64, _f, _i, _vp]
             for fn in (L.mrn_rmsnorm, L.mrn_rmsnorm_then_add, L.mrn_norm_residual_norm,
                        L.mrn_add_rmsnorm, L.mrn_rmsnorm_then_add_scale, L.mrn_rmsnorm_q8_1,
-                       L.mrn_rmsnorm_seam, L.mrn_rmsnorm_unweighted, L.mrn_seam_scale):
+                       L.mrn_rmsnorm_seam, L.mrn_rmsnorm_unweighted, L.mrn_seam_scale,
+                       L.mrn_layernorm, L.mrn_dropout_add, L.mrn_dropout_add_layernorm,
+                       L.mrn_norm_backward_workspace, L.mrn_layernorm_backward,
+                       L.mrn_dropout_add_layernorm_backward, L.mrn_rmsnorm_backward):
                 fn.restype = _i
             L.mrn_status_string.argtypes = [_i]
             L.mrn_status_string.restype = ctypes.c_char_p
@@ -184,6 +199,49 @@ def mrn_rmsnorm_unweighted(x, u, rows, n, eps, dtype, seam, stream=0) -> int:
 
 def mrn_seam_scale(u, gamma, y, rows, n, seam, stream=0) -> int:
     return lib().mrn_seam_scale(u, gamma, y, rows, n, seam, stream)
+
+
+def mrn_layernorm(x, gamma, beta, y, mean, rstd, rows, n, eps, dtype, stream=0) -> int:
+    return lib().mrn_layernorm(x, gamma, beta, y, mean, rstd, rows, n, eps, dtype, stream)
+
+
+def mrn_dropout_add(x, residual, out, rng, site, p, rows, n, dtype, stream=0) -> int:
+    return lib().mrn_dropout_add(x, residual, out, rng, site, p, rows, n, dtype, stream)
+
+
+def mrn_dropout_add_layernorm(x, residual, gamma, beta, out_stream, normed, mean, rstd, rng, site,
+                              p, rows, n, eps, dtype, stream=0) -> int:
+    return lib().mrn_dropout_add_layernorm(x, residual, gamma, beta, out_stream, normed, mean, rstd,
+                                           rng, site, p, rows, n, eps, dtype, stream)
+
+
+def mrn_norm_backward_workspace(rows, n) -> int:
+    """Bytes of workspace that a gradient of rows x n needs on the current device."""
+    out = ctypes.c_int64(0)
+    st = lib().mrn_norm_backward_workspace(rows, n, ctypes.byref(out))
+    if st != 0:
+        raise MrnError(st, "mrn_norm_backward_workspace")
+    return out.value
+
+
+def mrn_layernorm_backward(dy, x, gamma, mean, rstd, dstream, dx, dgamma, dbeta, workspace,
+                           workspace_bytes, rows, n, dtype, stream=0) -> int:
+    return lib().mrn_layernorm_backward(dy, x, gamma, mean, rstd, dstream, dx, dgamma, dbeta,
+                                        workspace, workspace_bytes, rows, n, dtype, stream)
+
+
+def mrn_dropout_add_layernorm_backward(dnormed, out_stream, gamma, mean, rstd, dstream, dx,
+                                       dresidual, dgamma, dbeta, rng, site, p, workspace,
+                                       workspace_bytes, rows, n, dtype, stream=0) -> int:
+    return lib().mrn_dropout_add_layernorm_backward(
+        dnormed, out_stream, gamma, mean, rstd, dstream, dx, dresidual, dgamma, dbeta, rng, site, p,
+        workspace, workspace_bytes, rows, n, dtype, stream)
+
+
+def mrn_rmsnorm_backward(dy, x, gamma, dstream, dx, dgamma, workspace, workspace_bytes, rows, n,
+                         eps, dtype, stream=0) -> int:
+    return lib().mrn_rmsnorm_backward(dy, x, gamma, dstream, dx, dgamma, workspace,
+                                      workspace_bytes, rows, n, eps, dtype, stream)
 
 
 def mrn_status_string(status: int) -> str:
@@ -441,3 +499,214 @@ def seam_scale(u, gamma, out=None):
     if st != 0:
         raise MrnError(st, "mrn_seam_scale")
     return out
+
+
+# ---------------------------------------------------------------------------
+# Training: LayerNorm, dropout before the residual add, and the gradients.  All
+# tensors of a call are on one device, which need not be the current one; the
+# work runs on that device's current stream.
+# ---------------------------------------------------------------------------
+def _train_rows(x, name):
+    """(rows, n, dtype code) of the tensor that fixes a call's shape, type and device."""
+    dt = _dtype_code(x)
+    _check(x, name, x.dtype)
+    if x.dim() == 0:
+        raise ValueError(f"{name} must have at least one dimension")
+    rows, n = _rows_n(x)
+    return rows, n, dt
+
+
+def _train_check(t, name, like, dtype, shape):
+    _check(t, name, dtype, shape)
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+
+
+def _ptr(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _rng_ptr(rng, like, p):
+    """rng: int64 or uint64 tensor {seed, offset} on the device; None when p == 0."""
+    import torch
+    if rng is None:
+        if p != 0:
+            raise ValueError("rng is required when p > 0")
+        return 0
+    if rng.dtype not in (torch.int64, torch.uint64):
+        raise TypeError(f"rng has dtype {rng.dtype}, expected int64 or uint64")
+    _train_check(rng, "rng", like, rng.dtype, (2,))
+    return rng.data_ptr()
+
+
+def _run(what, like, fn, *args):
+    """fn(*args, stream) on like's device and that device's current stream."""
+    import torch
+    if like.device.index == torch.cuda.current_device():
+        st = fn(*args, _stream(like))
+    else:
+        with torch.cuda.device(like.device):
+            st = fn(*args, _stream(like))
+    if st != 0:
+        raise MrnError(st, what)
+
+
+def _stats(mean, rstd, like, rows):
+    import torch
+    if (mean is None) != (rstd is None):
+        raise ValueError("mean and rstd are given together or not at all")
+    if mean is not None:
+        for t, name in ((mean, "mean"), (rstd, "rstd")):
+            _check(t, name, torch.float32)
+            if t.device != like.device or t.numel() != rows:
+                raise ValueError(f"{name} must hold one value per row ({rows}) on {like.device}")
+
+
+def norm_backward_workspace(x):
+    """Workspace (uint8 tensor) for the gradients of norms over x's last dimension,
+    on x's device.  Reusable by later calls of this shape on one stream; calls that
+    may run at the same time need one each."""
+    import torch
+    rows, n, _ = _train_rows(x, "x")
+    with torch.cuda.device(x.device):
+        return torch.empty(mrn_norm_backward_workspace(rows, n), dtype=torch.uint8,
+                           device=x.device)
+
+
+def _workspace(workspace, x):
+    import torch
+    if workspace is None:
+        return norm_backward_workspace(x)
+    _check(workspace, "workspace", torch.uint8)
+    if workspace.device != x.device:
+        raise ValueError(f"workspace is on {workspace.device}, expected {x.device}")
+    return workspace
+
+
+def layernorm(x, gamma, beta, eps: float, out=None, mean=None, rstd=None):
+    """LayerNorm over the last dimension; beta may be None, out may be x.  mean and
+    rstd (float32, one per row), when given, receive the row statistics that
+    layernorm_backward takes."""
+    import torch
+    rows, n, dt = _train_rows(x, "x")
+    _train_check(gamma, "gamma", x, x.dtype, (n,))
+    if beta is not None:
+        _train_check(beta, "beta", x, x.dtype, (n,))
+    _stats(mean, rstd, x, rows)
+    out = torch.empty_like(x) if out is None else out
+    _train_check(out, "out", x, x.dtype, x.shape)
+    _run("mrn_layernorm", x, mrn_layernorm, x.data_ptr(), gamma.data_ptr(), _ptr(beta),
+         out.data_ptr(), _ptr(mean), _ptr(rstd), rows, n, eps, dt)
+    return out
+
+
+def dropout_add(x, residual, p: float, rng, site: int = 0, out=None):
+    """residual + dropout(x); residual None gives dropout(x) alone, which is also the
+    gradient's form.  rng: device tensor {seed, offset}; out may be x or residual."""
+    import torch
+    rows, n, dt = _train_rows(x, "x")
+    if residual is not None:
+        _train_check(residual, "residual", x, x.dtype, x.shape)
+    out = torch.empty_like(x) if out is None else out
+    _train_check(out, "out", x, x.dtype, x.shape)
+    _run("mrn_dropout_add", x, mrn_dropout_add, x.data_ptr(), _ptr(residual), out.data_ptr(),
+         _rng_ptr(rng, x, p), site, p, rows, n, dt)
+    return out
+
+
+def dropout_add_layernorm(x, residual, gamma, beta, eps: float, p: float, rng, site: int = 0,
+                          out_stream=None, normed=None, mean=None, rstd=None):
+    """(out_stream, normed): out_stream = residual + dropout(x), normed =
+    layernorm(out_stream).  out_stream may be x or residual (in place)."""
+    import torch
+    rows, n, dt = _train_rows(x, "x")
+    _train_check(residual, "residual", x, x.dtype, x.shape)
+    _train_check(gamma, "gamma", x, x.dtype, (n,))
+    if beta is not None:
+        _train_check(beta, "beta", x, x.dtype, (n,))
+    _stats(mean, rstd, x, rows)
+    out_stream = torch.empty_like(x) if out_stream is None else out_stream
+    normed = torch.empty_like(x) if normed is None else normed
+    _train_check(out_stream, "out_stream", x, x.dtype, x.shape)
+    _train_check(normed, "normed", x, x.dtype, x.shape)
+    _run("mrn_dropout_add_layernorm", x, mrn_dropout_add_layernorm, x.data_ptr(),
+         residual.data_ptr(), gamma.data_ptr(), _ptr(beta), out_stream.data_ptr(),
+         normed.data_ptr(), _ptr(mean), _ptr(rstd), _rng_ptr(rng, x, p), site, p, rows, n, eps, dt)
+    return out_stream, normed
+
+
+def _backward_operands(dy, x, gamma, dstream, dx, dgamma):
+    import torch
+    rows, n, dt = _train_rows(x, "x")
+    _train_check(dy, "dy", x, x.dtype, x.shape)
+    _train_check(gamma, "gamma", x, x.dtype, (n,))
+    if dstream is not None:
+        _train_check(dstream, "dstream", x, x.dtype, x.shape)
+    dx = torch.empty_like(x) if dx is None else dx
+    _train_check(dx, "dx", x, x.dtype, x.shape)
+    if dgamma is None:
+        dgamma = torch.empty(n, dtype=torch.float32, device=x.device)
+    _train_check(dgamma, "dgamma", x, torch.float32, (n,))
+    return rows, n, dt, dx, dgamma
+
+
+def _dbeta(dbeta, bias, x, n):
+    import torch
+    if not bias:
+        return None
+    if dbeta is None:
+        dbeta = torch.empty(n, dtype=torch.float32, device=x.device)
+    _train_check(dbeta, "dbeta", x, torch.float32, (n,))
+    return dbeta
+
+
+def _need_stats(mean, rstd, x, rows):
+    if mean is None or rstd is None:
+        raise ValueError("mean and rstd of the forward pass are required")
+    _stats(mean, rstd, x, rows)
+
+
+def layernorm_backward(dy, x, gamma, mean, rstd, dstream=None, dx=None, dgamma=None, dbeta=None,
+                       bias: bool = True, workspace=None):
+    """(dx, dgamma, dbeta) of layernorm; dgamma and dbeta are float32, dbeta is None
+    when bias is false.  dstream, when given, is added to dx; dx may be dy, x or
+    dstream.  workspace: norm_backward_workspace(x), allocated here when None."""
+    rows, n, dt, dx, dgamma = _backward_operands(dy, x, gamma, dstream, dx, dgamma)
+    _need_stats(mean, rstd, x, rows)
+    dbeta = _dbeta(dbeta, bias, x, n)
+    ws = _workspace(workspace, x)
+    _run("mrn_layernorm_backward", x, mrn_layernorm_backward, dy.data_ptr(), x.data_ptr(),
+         gamma.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ptr(dstream), dx.data_ptr(),
+         dgamma.data_ptr(), _ptr(dbeta), ws.data_ptr(), ws.numel(), rows, n, dt)
+    return dx, dgamma, dbeta
+
+
+def dropout_add_layernorm_backward(dnormed, out_stream, gamma, mean, rstd, p: float, rng,
+                                   site: int = 0, dstream=None, dx=None, dresidual=None,
+                                   dgamma=None, dbeta=None, bias: bool = True, workspace=None):
+    """(dx, dresidual, dgamma, dbeta) of dropout_add_layernorm, from its out_stream,
+    mean, rstd and the same p, rng values and site."""
+    import torch
+    rows, n, dt, dx, dgamma = _backward_operands(dnormed, out_stream, gamma, dstream, dx, dgamma)
+    _need_stats(mean, rstd, out_stream, rows)
+    dresidual = torch.empty_like(out_stream) if dresidual is None else dresidual
+    _train_check(dresidual, "dresidual", out_stream, out_stream.dtype, out_stream.shape)
+    dbeta = _dbeta(dbeta, bias, out_stream, n)
+    ws = _workspace(workspace, out_stream)
+    _run("mrn_dropout_add_layernorm_backward", out_stream, mrn_dropout_add_layernorm_backward,
+         dnormed.data_ptr(), out_stream.data_ptr(), gamma.data_ptr(), mean.data_ptr(),
+         rstd.data_ptr(), _ptr(dstream), dx.data_ptr(), dresidual.data_ptr(), dgamma.data_ptr(),
+         _ptr(dbeta), _rng_ptr(rng, out_stream, p), site, p, ws.data_ptr(), ws.numel(), rows, n, dt)
+    return dx, dresidual, dgamma, dbeta
+
+
+def rmsnorm_backward(dy, x, gamma, eps: float, dstream=None, dx=None, dgamma=None,
+                     workspace=None):
+    """(dx, dgamma) of rmsnorm; dgamma is float32.  dstream, when given, is added to
+    dx; dx may be dy, x or dstream."""
+    rows, n, dt, dx, dgamma = _backward_operands(dy, x, gamma, dstream, dx, dgamma)
+    ws = _workspace(workspace, x)
+    _run("mrn_rmsnorm_backward", x, mrn_rmsnorm_backward, dy.data_ptr(), x.data_ptr(),
+         gamma.data_ptr(), _ptr(dstream), dx.data_ptr(), dgamma.data_ptr(), ws.data_ptr(),
+         ws.numel(), rows, n, eps, dt)
+    return dx, dgamma

@@ -15,6 +15,9 @@
  *   mrn_add_rmsnorm, mrn_rmsnorm_then_add_scale, mrn_rmsnorm_q8_1 (Hesper
  *   "RMSNorm Layer" kernels) and the split-norm seam mrn_rmsnorm_seam,
  *   mrn_rmsnorm_unweighted, mrn_seam_scale ("Chapter 12", section 12.7).
+ * For training: mrn_layernorm, mrn_dropout_add, mrn_dropout_add_layernorm and the
+ *   gradients mrn_layernorm_backward, mrn_dropout_add_layernorm_backward,
+ *   mrn_rmsnorm_backward.
  *
  * Sources: "Chapter 12 -- RMSNorm and the dual-epsilon sandwich" section 12.1
  * (definition), 12.2 (two epsilons: 1e-8 for the post norms, 1e-5 for the pre
@@ -91,8 +94,10 @@ typedef enum mrn_dtype {
 typedef enum mrn_status {
     MRN_OK = 0,
     MRN_ERR_NULL_POINTER = 1,      /* a required pointer is NULL (rows > 0) */
-    MRN_ERR_INVALID_SIZE = 2,      /* n < 1, rows < 0, or rows*n*size overflows */
-    MRN_ERR_INVALID_EPS = 3,       /* eps not finite or not > 0 */
+    MRN_ERR_INVALID_SIZE = 2,      /* n < 1, rows < 0, rows*n*size overflows, or a
+                                      workspace smaller than the call needs */
+    MRN_ERR_INVALID_EPS = 3,       /* eps not finite or not > 0, or a dropout
+                                      probability outside 0 .. 1 */
     MRN_ERR_UNSUPPORTED_DTYPE = 4, /* dtype not MRN_F32 / MRN_BF16 (seam format not
                                       MRN_F16 / MRN_BF16) */
     MRN_ERR_ALIASING = 5,          /* a forbidden overlap between buffers */
@@ -229,6 +234,132 @@ mrn_status mrn_rmsnorm_unweighted(const void *x, void *u, int64_t rows, int64_t 
                                   mrn_dtype dtype, mrn_dtype seam, cudaStream_t stream);
 mrn_status mrn_seam_scale(const void *u, const void *gamma, void *y, int64_t rows, int64_t n,
                           mrn_dtype seam, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Training: LayerNorm, dropout before the residual add, and the gradients of
+ * LayerNorm and RMSNorm.  Not on the pages, which only run a model.  The
+ * conventions above hold (pointers, layout, dtype, alignment, aliasing, stream,
+ * errors); rows == 0 is a no-op except where a gradient of weights is due,
+ * which is then zero.  Rows need no alignment beyond the element's, but rows
+ * whose operands all sit at one offset within 16 bytes are moved in 16-byte
+ * granules as described above.
+ *
+ * Dropout and its generator
+ *   Element e = r*n + j of the flattened matrix is kept when u16(e) >= t, with
+ *   t = round(p * 2^16), and kept values are multiplied by 2^16 / (2^16 - t) (the
+ *   exact inverse of the probability kept; 0 when t = 2^16).  p is a double in
+ *   0 .. 1, taken to the nearest multiple of 2^-16.  u16(e) is 16-bit lane e % 8 (low half
+ *   of each word first) of Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel
+ *   random numbers: as easy as 1, 2, 3", 2011) with key rng[0] and counter
+ *   (e / 8, rng[1] + site), 64 bits each, the lower words e / 8.
+ *   rng is device memory, read when the kernel runs: a captured graph draws new
+ *   masks at each replay when rng[1] is advanced between replays.  Call sites
+ *   that share rng within a step take different `site`s, and rng[1] is advanced
+ *   past the largest.  The mask is never stored: a gradient evaluates it again
+ *   from the same rng values, site, p and shape.  A dropped value does not reach
+ *   the result, whatever it is (infinities and NaN included).  rng may be NULL
+ *   when t = 0.
+ */
+
+/*
+ * LayerNorm of every row:
+ *   mean = sum_j x[r,j] / n,  rstd = 1 / sqrt(sum_j (x[r,j] - mean)^2 / n + eps)
+ *   y[r,j] = (x[r,j] - mean) * rstd * gamma[j] + beta[j]
+ *   x           [rows x n]
+ *   gamma       [n]
+ *   beta        [n]         or NULL (no bias)
+ *   y           [rows x n]  may be x itself
+ *   mean, rstd  [rows]      f32, the row statistics kept for the gradient; both or
+ *                           neither NULL
+ * The variance is summed from the deviations in f32, not from the squares.
+ */
+mrn_status mrn_layernorm(const void *x, const void *gamma, const void *beta, void *y,
+                         float *mean, float *rstd, int64_t rows, int64_t n, float eps,
+                         mrn_dtype dtype, cudaStream_t stream);
+
+/*
+ * Dropout, then the residual add, in one kernel:
+ *   out[r,j] = residual[r,j] + dropout(x)[r,j]        (one rounding)
+ *   residual  [rows x n]  or NULL: out = dropout(x), which is also the gradient's
+ *                         own form (dx = dropout(dout))
+ *   out       [rows x n]  may be x or residual
+ */
+mrn_status mrn_dropout_add(const void *x, const void *residual, void *out,
+                           const uint64_t *rng, uint64_t site, double p,
+                           int64_t rows, int64_t n, mrn_dtype dtype, cudaStream_t stream);
+
+/*
+ * The tail of a training sub-block in one kernel: dropout, residual add, and the
+ * LayerNorm of the new stream:
+ *   out_stream = residual + dropout(x), rounded once to dtype and stored
+ *   normed     = layernorm(out_stream as stored)
+ *   out_stream  [rows x n]  may be x or residual
+ *   normed      [rows x n]  may be x or residual, never overlapping out_stream
+ *   beta, mean, rstd as in mrn_layernorm.  p = 0 is the residual add and LayerNorm.
+ */
+mrn_status mrn_dropout_add_layernorm(const void *x, const void *residual, const void *gamma,
+                                     const void *beta, void *out_stream, void *normed,
+                                     float *mean, float *rstd, const uint64_t *rng,
+                                     uint64_t site, double p, int64_t rows, int64_t n, float eps,
+                                     mrn_dtype dtype, cudaStream_t stream);
+
+/*
+ * Bytes of the workspace of a gradient of rows x n (either norm, either dtype) on
+ * the current device.  The workspace is scratch: 16-byte aligned device memory that
+ * holds nothing between calls, used by the call's kernels until they have run.  Calls
+ * that may run at the same time (two streams, two graphs replayed together) need a
+ * workspace each.
+ */
+mrn_status mrn_norm_backward_workspace(int64_t rows, int64_t n, int64_t *bytes);
+
+/*
+ * Gradient of mrn_layernorm.  With xh = (x - mean) * rstd and w = dy * gamma:
+ *   dx[r,j]   = rstd * (w - sum_j w / n - xh * sum_j (w * xh) / n) + dstream[r,j]
+ *   dgamma[j] = sum_r dy * xh,   dbeta[j] = sum_r dy
+ *   dy          [rows x n]  gradient of y
+ *   x           [rows x n]  the forward's input;  mean, rstd [rows] f32, its statistics
+ *   dstream     [rows x n]  or NULL: the gradient that reaches x beside the norm (the
+ *                           residual stream's), added to dx
+ *   dx          [rows x n]  may be dy, x or dstream
+ *   dgamma      [n]         f32 whatever the dtype (a sum over all rows)
+ *   dbeta       [n]         f32, or NULL
+ * The sums over rows are taken in a fixed order: the same call gives the same bits.
+ * rows == 0 writes zeros to dgamma and dbeta; the other pointers are not read.
+ */
+mrn_status mrn_layernorm_backward(const void *dy, const void *x, const void *gamma,
+                                  const float *mean, const float *rstd, const void *dstream,
+                                  void *dx, float *dgamma, float *dbeta,
+                                  void *workspace, int64_t workspace_bytes,
+                                  int64_t rows, int64_t n, mrn_dtype dtype, cudaStream_t stream);
+
+/*
+ * Gradient of mrn_dropout_add_layernorm, with the forward's out_stream, mean, rstd,
+ * rng values, site and p:
+ *   ds        = layernorm gradient of dnormed at out_stream, + dstream
+ *   dresidual = ds                       (rounded once)
+ *   dx        = dropout(ds)              (from the f32 ds, rounded once)
+ *   dx, dresidual  [rows x n]  each may be dnormed, out_stream or dstream, not each other
+ */
+mrn_status mrn_dropout_add_layernorm_backward(
+    const void *dnormed, const void *out_stream, const void *gamma, const float *mean,
+    const float *rstd, const void *dstream, void *dx, void *dresidual, float *dgamma,
+    float *dbeta, const uint64_t *rng, uint64_t site, double p, void *workspace,
+    int64_t workspace_bytes, int64_t rows, int64_t n, mrn_dtype dtype, cudaStream_t stream);
+
+/*
+ * Gradient of mrn_rmsnorm (and, with dstream, of mrn_add_rmsnorm: both summands get
+ * dx; of mrn_norm_residual_norm: once at out_stream with gamma_pre and dstream, then
+ * once at block_out with gamma_post).  inv is recomputed from x, so no statistics are
+ * kept.  With w = dy * gamma:
+ *   dx[r,j]   = inv * (w - x * inv^2 * sum_j (w * x) / n) + dstream[r,j]
+ *   dgamma[j] = sum_r dy * x * inv
+ * Operands as in mrn_layernorm_backward.
+ */
+mrn_status mrn_rmsnorm_backward(const void *dy, const void *x, const void *gamma,
+                                const void *dstream, void *dx, float *dgamma,
+                                void *workspace, int64_t workspace_bytes,
+                                int64_t rows, int64_t n, float eps,
+                                mrn_dtype dtype, cudaStream_t stream);
 
 /* Static, human-readable name of a status code; never NULL. */
 const char *mrn_status_string(mrn_status status);
