@@ -5,7 +5,7 @@
 //   y = (s - mean) * rstd * gamma + beta      (s the stored stream, or x)
 // The variance is summed from the deviations, not from the squares: a row
 // whose mean is far from zero loses no digits.
-#include "mrn_train_kernels.cuh"
+#include "mrn_row_tile.cuh"
 
 namespace mrn {
 
@@ -55,9 +55,164 @@ __global__ void __launch_bounds__(kLoopedThreads) mrn_layernorm_looped_kernel(co
     }
 }
 
+// The row held in registers between its copy and its outputs (see mrn_row_tile.cuh).
+template <class T, int K, bool EDGE, bool WARP, bool ADD>
+__global__ void __launch_bounds__(WARP ? 128 : tile_max_threads(K))
+mrn_layernorm_tile_kernel(const LayernormArgs a, const TileArgs t) {
+    extern __shared__ __align__(16) unsigned char ring_bytes[];
+    __shared__ RowSumSlots<1> slots;
+    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(ring_bytes));
+    const RowTile<T, K, EDGE, WARP> tile(a.rows, a.n, t);
+    constexpr int kOps = ADD ? 2 : 1;
+    const int64_t back = static_cast<int64_t>(t.mis) * T::kBytes;
+    const char *const ops[kTileMaxOperands] = {static_cast<const char *>(a.x) - back,
+                                               ADD ? static_cast<const char *>(a.res) - back : nullptr,
+                                               nullptr};
+    char *const y = static_cast<char *>(a.y) - back;
+    char *const stream_out = ADD ? static_cast<char *>(a.stream_out) - back : nullptr;
+    uint32_t in[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) in[k] = tile.inside(k);
+    if (tile.cl > 1) cluster_arrive_relaxed();   // (peers' shared memory is written later)
+    pdl_enter();
+    const int ahead = t.stages - 1;
+    for (int s = 0; s < ahead; ++s) {
+        const int64_t r = tile.row + s * tile.stride;
+        tile.issue(ring, s, r, r < a.rows, ops, kOps);
+        cp_async_commit();
+    }
+    const DropKey key = ADD ? drop_key(a.drop) : DropKey{};
+    Slot<T> gamma[K], beta[K];
+    tile.weights(gamma, in, a.gamma);
+    if (a.beta) {
+        tile.weights(beta, in, a.beta);
+    } else {
+#pragma unroll
+        for (int k = 0; k < K; ++k) beta[k].zero();
+    }
+    if (tile.cl > 1) cluster_wait_acquire();
+    const float count = static_cast<float>(a.n);
+    int turn = 0, stage = 0, fill = ahead;
+    for (int64_t it = 0; tile.cta_row(it) < a.rows; ++it) {
+        const int64_t r = tile.row + it * tile.stride;
+        const bool ok = r < a.rows;
+        __syncwarp();
+        const int64_t next = r + ahead * tile.stride;
+        tile.issue(ring, fill, next, next < a.rows, ops, kOps);
+        cp_async_commit();
+        fill = fill + 1 == t.stages ? 0 : fill + 1;
+        cp_async_wait(ahead);
+        __syncwarp();
+        Slot<T> v[K];
+        tile.fetch(v, ring, stage, 0, kOps);
+        tile.mask(v, in);
+        if constexpr (ADD) {
+            Slot<T> res[K];
+            tile.fetch(res, ring, stage, 1, kOps);
+            tile.mask(res, in);
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                if (in[k] == 0u) continue;
+                uint32_t w[4] = {0u, 0u, 0u, 0u};
+                if (a.drop.threshold != 0u)
+                    philox_lanes(key, static_cast<uint64_t>((tile.slot0(r) >> 3) + tile.first +
+                                                            k * tile.width), w);
+                float o[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    o[i] = drop_add(v[k].get(i), res[k].get(i), drop_keeps(w, i, a.drop.threshold),
+                                    a.drop.scale);
+                v[k].put(o);
+                if (ok) tile.store(stream_out, r, k, in[k], v[k]);
+            }
+        }
+        stage = stage + 1 == t.stages ? 0 : stage + 1;
+        float sum[1] = {0.0f};
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[0] += v[k].get(i);
+        }
+        row_sum<1, WARP>(sum, slots, turn, tile.width, tile.cl, tile.crank);
+        const float mean = sum[0] / count;
+        float dev[1] = {0.0f};
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (in[k] == 0u) continue;
+            if (!EDGE || in[k] == 0xFFu) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float d = v[k].get(i) - mean;
+                    dev[0] = fmaf(d, d, dev[0]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float d = ((in[k] >> i) & 1u) ? v[k].get(i) - mean : 0.0f;
+                    dev[0] = fmaf(d, d, dev[0]);
+                }
+            }
+        }
+        row_sum<1, WARP>(dev, slots, turn, tile.width, tile.cl, tile.crank);
+        const float rstd = 1.0f / sqrtf(dev[0] / count + a.eps);
+        if (ok) {
+            if (a.mean && tile.first == 0) {
+                a.mean[r] = mean;
+                a.rstd[r] = rstd;
+            }
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                float o[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    o[i] = fmaf((v[k].get(i) - mean) * rstd, gamma[k].get(i), beta[k].get(i));
+                Slot<T> out;
+                out.put(o);
+                tile.store(y, r, k, in[k], out);
+            }
+        }
+    }
+    cp_async_wait(0);
+}
+
+template <class T, int K, bool EDGE, bool WARP, bool ADD>
+cudaError_t launch_layernorm_tile(const LayernormArgs &a, const TilePlan &p, bool pdl,
+                                  cudaStream_t stream, uint64_t *launches) {
+    static TileLaunchCache cache;
+    const TileArgs t = {p.lanes, p.stages, p.mis};
+    const int64_t shared = tile_ring_bytes(T::kBytes, K, p.threads, p.stages, ADD ? 2 : 1);
+    return launch_tile(cache, mrn_layernorm_tile_kernel<T, K, EDGE, WARP, ADD>, p, shared, pdl,
+                       stream, launches, a, t);
+}
+
+template <class T, int K, bool WARP>
+cudaError_t launch_layernorm_k(const LayernormArgs &a, const TilePlan &p, bool pdl,
+                               cudaStream_t stream, uint64_t *launches) {
+    if (a.res)
+        return p.edge ? launch_layernorm_tile<T, K, true, WARP, true>(a, p, pdl, stream, launches)
+                      : launch_layernorm_tile<T, K, false, WARP, true>(a, p, pdl, stream, launches);
+    return p.edge ? launch_layernorm_tile<T, K, true, WARP, false>(a, p, pdl, stream, launches)
+                  : launch_layernorm_tile<T, K, false, WARP, false>(a, p, pdl, stream, launches);
+}
+
 template <class T>
 cudaError_t launch_layernorm_typed(const LayernormArgs &a, int sms, bool pdl, cudaStream_t stream,
                                    uint64_t *launches) {
+    const int mis = common_offset(T::kBytes, a.x, a.y, a.res, static_cast<const void *>(a.stream_out));
+    // (a generator group is a slot only when the operands start on a slot boundary)
+    if (mis == 0 || (mis > 0 && a.drop.threshold == 0)) {
+        const TileWish wish = {a.res ? 2 : 1, 1024, 8};
+        const TilePlan p = plan_tiles(a.rows, a.n, T::kBytes, mis, wish, sms);
+        if (p.ok && p.warp) {
+            if (p.k == 1) return launch_layernorm_k<T, 1, true>(a, p, pdl, stream, launches);
+            if (p.k == 2) return launch_layernorm_k<T, 2, true>(a, p, pdl, stream, launches);
+            return launch_layernorm_k<T, 4, true>(a, p, pdl, stream, launches);
+        }
+        if (p.ok) {
+            if (p.k == 1) return launch_layernorm_k<T, 1, false>(a, p, pdl, stream, launches);
+            return launch_layernorm_k<T, 2, false>(a, p, pdl, stream, launches);
+        }
+    }
     const int64_t ctas = a.rows < 4LL * sms ? a.rows : 4LL * sms;
     return launch_plain(mrn_layernorm_looped_kernel<T>, ctas, kLoopedThreads, 0, pdl, stream,
                         launches, a);

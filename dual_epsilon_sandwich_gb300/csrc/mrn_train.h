@@ -63,8 +63,8 @@ cudaError_t launch_layernorm(bool bf16, const LayernormArgs &a, int sms, bool pd
                              cudaStream_t stream, uint64_t *launches);
 cudaError_t launch_norm_backward(bool bf16, const BackwardArgs &a, int sms, bool pdl,
                                  cudaStream_t stream, uint64_t *launches);
-cudaError_t launch_dropout(bool bf16, const DropoutArgs &a, int sms, bool pdl,
-                           cudaStream_t stream, uint64_t *launches);
+cudaError_t launch_dropout(bool bf16, const DropoutArgs &a, bool pdl, cudaStream_t stream,
+                           uint64_t *launches);
 
 // Partial sums of dgamma (and of dbeta) that a backward pass keeps at most: the
 // rows of [parts x n] floats in its workspace, for each of the two.

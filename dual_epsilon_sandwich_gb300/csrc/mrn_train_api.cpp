@@ -280,8 +280,7 @@ mrn_status mrn_dropout_add(const void *x, const void *residual, void *out, const
     a.y = out;
     a.total = rows * n;
     uint64_t launched = 0;
-    const cudaError_t err = launch_dropout(dtype == MRN_BF16, a, sm_count_of_current_device(),
-                                           launch_pdl(), stream, &launched);
+    const cudaError_t err = launch_dropout(dtype == MRN_BF16, a, launch_pdl(), stream, &launched);
     return launch_result(err, launched);
 }
 

@@ -130,6 +130,74 @@ cudaError_t launch_plain(void (*fn)(Params...), int64_t ctas, int threads, size_
     return err;
 }
 
+// ---------------------------------------------------------------------------
+// Eight consecutive elements of one operand, as raw bits: the share of one
+// thread in a row, and the elements of one generator group.  16 bytes of bf16;
+// 32 bytes of f32, moved in one 256-bit access.
+// ---------------------------------------------------------------------------
+template <class T> struct Slot {
+    static constexpr int kWords = 2 * T::kBytes;
+    uint32_t w[kWords];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = 0u;
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (T::kBytes == 4) {
+            return __uint_as_float(w[i]);
+        } else {
+            const uint32_t u = w[i >> 1];
+            return __uint_as_float((i & 1) ? (u & 0xFFFF0000u) : (u << 16));
+        }
+    }
+    // rounds to T (to nearest even)
+    __device__ __forceinline__ void put(const float (&f)[8]) {
+        if constexpr (T::kBytes == 4) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(f[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+        }
+    }
+    __device__ __forceinline__ void clear(int i) {
+        if constexpr (T::kBytes == 4) {
+            w[i] = 0u;
+        } else {
+            w[i >> 1] &= (i & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+        }
+    }
+    __device__ __forceinline__ void st_one(char *p, int i) const {
+        if constexpr (T::kBytes == 4) {
+            asm volatile("st.global.u32 [%0], %1;" :: "l"(p), "r"(w[i]) : "memory");
+        } else {
+            const unsigned short h =
+                static_cast<unsigned short>((i & 1) ? (w[i >> 1] >> 16) : (w[i >> 1] & 0xFFFFu));
+            asm volatile("st.global.u16 [%0], %1;" :: "l"(p), "h"(h) : "memory");
+        }
+    }
+};
+
+// A whole slot, aligned to its size; read once (past L1).
+__device__ __forceinline__ void ld_slot(Slot<BF16> &s, const void *p) {
+    asm volatile("ld.global.L1::no_allocate.L2::256B.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(s.w[0]), "=r"(s.w[1]), "=r"(s.w[2]), "=r"(s.w[3]) : "l"(p));
+}
+__device__ __forceinline__ void ld_slot(Slot<F32> &s, const void *p) {
+    asm volatile("ld.global.L1::no_allocate.L2::256B.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(s.w[0]), "=r"(s.w[1]), "=r"(s.w[2]), "=r"(s.w[3]), "=r"(s.w[4]),
+                   "=r"(s.w[5]), "=r"(s.w[6]), "=r"(s.w[7]) : "l"(p));
+}
+__device__ __forceinline__ void st_slot(void *p, const Slot<BF16> &s) {
+    asm volatile("st.global.v4.b32 [%0], {%1,%2,%3,%4};"
+                 :: "l"(p), "r"(s.w[0]), "r"(s.w[1]), "r"(s.w[2]), "r"(s.w[3]) : "memory");
+}
+__device__ __forceinline__ void st_slot(void *p, const Slot<F32> &s) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 :: "l"(p), "r"(s.w[0]), "r"(s.w[1]), "r"(s.w[2]), "r"(s.w[3]), "r"(s.w[4]),
+                    "r"(s.w[5]), "r"(s.w[6]), "r"(s.w[7]) : "memory");
+}
+
 // One element of T at p.
 template <class T> __device__ __forceinline__ float ld_elem(const void *base, int64_t e) {
     Frag<T, 1> f;
