@@ -37,13 +37,12 @@ __global__ void __launch_bounds__(kDropoutThreads) mrn_dropout_kernel(const Drop
             const int64_t g = g0 + k * kDropoutThreads;
             const int64_t e = g * 8;
             if (e >= a.total) continue;
-            uint32_t w[4] = {0u, 0u, 0u, 0u};
-            if (a.drop.threshold != 0u) philox_lanes(key, static_cast<uint64_t>(g), w);
+            const DropGroup d = drop_group(key, static_cast<uint64_t>(g), a.drop.threshold);
             if (VEC && e + 8 <= a.total) {
                 float o[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const bool keep = drop_keeps(w, i, a.drop.threshold);
+                    const bool keep = d.keeps(i);
                     o[i] = ADD ? drop_add(x[k].get(i), r[k].get(i), keep, a.drop.scale)
                                : drop_scale(x[k].get(i), keep, a.drop.scale);
                 }
@@ -53,7 +52,7 @@ __global__ void __launch_bounds__(kDropoutThreads) mrn_dropout_kernel(const Drop
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     if (e + i >= a.total) break;
-                    const bool keep = drop_keeps(w, i, a.drop.threshold);
+                    const bool keep = d.keeps(i);
                     const float v = ld_elem<T>(a.x, e + i);
                     st_elem<T>(a.y, e + i,
                                ADD ? drop_add(v, ld_elem<T>(a.res, e + i), keep, a.drop.scale)

@@ -62,7 +62,7 @@ mrn_layernorm_tile_kernel(const LayernormArgs a, const TileArgs t) {
     extern __shared__ __align__(16) unsigned char ring_bytes[];
     __shared__ RowSumSlots<1> slots;
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(ring_bytes));
-    const RowTile<T, K, EDGE, WARP> tile(a.rows, a.n, t);
+    RowTile<T, K, EDGE, WARP> tile(a.rows, a.n, t);
     constexpr int kOps = ADD ? 2 : 1;
     const int64_t back = static_cast<int64_t>(t.mis) * T::kBytes;
     const char *const ops[kTileMaxOperands] = {static_cast<const char *>(a.x) - back,
@@ -70,105 +70,94 @@ mrn_layernorm_tile_kernel(const LayernormArgs a, const TileArgs t) {
                                                nullptr};
     char *const y = static_cast<char *>(a.y) - back;
     char *const stream_out = ADD ? static_cast<char *>(a.stream_out) - back : nullptr;
-    uint32_t in[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) in[k] = tile.inside(k);
+    RingWalk walk(kOps * K * tile.region, t.stages);
+    const int ahead = t.stages - 1;
+    tile.clear(ring, t.stages, kOps);
     if (tile.cl > 1) cluster_arrive_relaxed();   // (peers' shared memory is written later)
     pdl_enter();
-    const int ahead = t.stages - 1;
-    for (int s = 0; s < ahead; ++s) {
-        const int64_t r = tile.row + s * tile.stride;
-        tile.issue(ring, s, r, r < a.rows, ops, kOps);
-        cp_async_commit();
-    }
+    for (int s = 0; s < ahead; ++s) tile.issue(ring + s * walk.bytes, s, ops, kOps);
     const DropKey key = ADD ? drop_key(a.drop) : DropKey{};
     Slot<T> gamma[K], beta[K];
-    tile.weights(gamma, in, a.gamma);
+    tile.weights(gamma, a.gamma);
     if (a.beta) {
-        tile.weights(beta, in, a.beta);
+        tile.weights(beta, a.beta);
     } else {
 #pragma unroll
         for (int k = 0; k < K; ++k) beta[k].zero();
     }
     if (tile.cl > 1) cluster_wait_acquire();
-    const float count = static_cast<float>(a.n);
-    int turn = 0, stage = 0, fill = ahead;
-    for (int64_t it = 0; tile.cta_row(it) < a.rows; ++it) {
-        const int64_t r = tile.row + it * tile.stride;
-        const bool ok = r < a.rows;
+    const float inv_n = 1.0f / static_cast<float>(a.n);
+    int turn = 0;
+    for (; tile.cta_row() < a.rows; tile.advance(), walk.next()) {
         __syncwarp();
-        const int64_t next = r + ahead * tile.stride;
-        tile.issue(ring, fill, next, next < a.rows, ops, kOps);
-        cp_async_commit();
-        fill = fill + 1 == t.stages ? 0 : fill + 1;
+        tile.issue(ring + walk.write * walk.bytes, ahead, ops, kOps);
         cp_async_wait(ahead);
         __syncwarp();
+        const uint32_t from = ring + walk.read * walk.bytes;
         Slot<T> v[K];
-        tile.fetch(v, ring, stage, 0, kOps);
-        tile.mask(v, in);
+        tile.fetch(v, from, 0);
         if constexpr (ADD) {
             Slot<T> res[K];
-            tile.fetch(res, ring, stage, 1, kOps);
-            tile.mask(res, in);
+            tile.fetch(res, from, 1);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                if (in[k] == 0u) continue;
-                uint32_t w[4] = {0u, 0u, 0u, 0u};
-                if (a.drop.threshold != 0u)
-                    philox_lanes(key, static_cast<uint64_t>((tile.slot0(r) >> 3) + tile.first +
-                                                            k * tile.width), w);
+                if (tile.in[k] == 0u) continue;
+                const DropGroup d = drop_group(key, tile.group(k), a.drop.threshold);
                 float o[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    o[i] = drop_add(v[k].get(i), res[k].get(i), drop_keeps(w, i, a.drop.threshold),
-                                    a.drop.scale);
+                    o[i] = drop_add(v[k].get(i), res[k].get(i), d.keeps(i), a.drop.scale);
                 v[k].put(o);
-                if (ok) tile.store(stream_out, r, k, in[k], v[k]);
+                if (!WARP || tile.row < a.rows) tile.store(stream_out, k, v[k]);
             }
         }
-        stage = stage + 1 == t.stages ? 0 : stage + 1;
-        float sum[1] = {0.0f};
+        uint64_t acc = 0;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum[0] += v[k].get(i);
+            for (int i = 0; i < 4; ++i) acc = f2_add(acc, v[k].pair(i));
         }
+        float sum[1] = {f2_sum(acc)};
         row_sum<1, WARP>(sum, slots, turn, tile.width, tile.cl, tile.crank);
-        const float mean = sum[0] / count;
-        float dev[1] = {0.0f};
+        const float mean = sum[0] * inv_n;
+        const uint64_t minus = f2_pack(-mean, -mean);
+        acc = 0;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            if (in[k] == 0u) continue;
-            if (!EDGE || in[k] == 0xFFu) {
+            if (tile.in[k] == 0u) continue;
+            if (!EDGE || tile.in[k] == 0xFFu) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float d = v[k].get(i) - mean;
-                    dev[0] = fmaf(d, d, dev[0]);
+                for (int i = 0; i < 4; ++i) {
+                    const uint64_t d = f2_add(v[k].pair(i), minus);
+                    acc = f2_fma(d, d, acc);
                 }
             } else {
+                float part = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float d = ((in[k] >> i) & 1u) ? v[k].get(i) - mean : 0.0f;
-                    dev[0] = fmaf(d, d, dev[0]);
+                    const float d = ((tile.in[k] >> i) & 1u) ? v[k].get(i) - mean : 0.0f;
+                    part = fmaf(d, d, part);
                 }
+                acc = f2_add(acc, f2_pack(part, 0.0f));
             }
         }
+        float dev[1] = {f2_sum(acc)};
         row_sum<1, WARP>(dev, slots, turn, tile.width, tile.cl, tile.crank);
-        const float rstd = 1.0f / sqrtf(dev[0] / count + a.eps);
-        if (ok) {
+        const float rstd = inv_sqrt(fmaf(dev[0], inv_n, a.eps));
+        if (!WARP || tile.row < a.rows) {
             if (a.mean && tile.first == 0) {
-                a.mean[r] = mean;
-                a.rstd[r] = rstd;
+                a.mean[tile.row] = mean;
+                a.rstd[tile.row] = rstd;
             }
+            const uint64_t scale = f2_pack(rstd, rstd);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                float o[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    o[i] = fmaf((v[k].get(i) - mean) * rstd, gamma[k].get(i), beta[k].get(i));
                 Slot<T> out;
-                out.put(o);
-                tile.store(y, r, k, in[k], out);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    out.put_pair(i, f2_fma(f2_mul(f2_add(v[k].pair(i), minus), scale),
+                                           gamma[k].pair(i), beta[k].pair(i)));
+                tile.store(y, k, out);
             }
         }
     }
@@ -201,7 +190,7 @@ cudaError_t launch_layernorm_typed(const LayernormArgs &a, int sms, bool pdl, cu
     const int mis = common_offset(T::kBytes, a.x, a.y, a.res, static_cast<const void *>(a.stream_out));
     // (a generator group is a slot only when the operands start on a slot boundary)
     if (mis == 0 || (mis > 0 && a.drop.threshold == 0)) {
-        const TileWish wish = {a.res ? 2 : 1, 1024, 8};
+        const TileWish wish = {a.res ? 2 : 1, 2, 1024, 8};
         const TilePlan p = plan_tiles(a.rows, a.n, T::kBytes, mis, wish, sms);
         if (p.ok && p.warp) {
             if (p.k == 1) return launch_layernorm_k<T, 1, true>(a, p, pdl, stream, launches);
@@ -210,7 +199,9 @@ cudaError_t launch_layernorm_typed(const LayernormArgs &a, int sms, bool pdl, cu
         }
         if (p.ok) {
             if (p.k == 1) return launch_layernorm_k<T, 1, false>(a, p, pdl, stream, launches);
-            return launch_layernorm_k<T, 2, false>(a, p, pdl, stream, launches);
+            if (p.k == 2) return launch_layernorm_k<T, 2, false>(a, p, pdl, stream, launches);
+            if (p.k == 3) return launch_layernorm_k<T, 3, false>(a, p, pdl, stream, launches);
+            return launch_layernorm_k<T, 4, false>(a, p, pdl, stream, launches);
         }
     }
     const int64_t ctas = a.rows < 4LL * sms ? a.rows : 4LL * sms;

@@ -34,14 +34,15 @@ int64_t backward_parts(int64_t rows, int64_t n, int sms) {
 // element of them read and written by one thread only.
 template <class T, bool RMS>
 __global__ void __launch_bounds__(kLoopedThreads)
-mrn_norm_backward_looped_kernel(const BackwardArgs a, float *part_gamma, float *part_beta) {
+mrn_norm_backward_looped_kernel(const BackwardArgs a, float *part_gamma, float *part_beta,
+                                const int64_t part_stride) {
     __shared__ CtaSumSlots<2> slots;
     pdl_enter();
     int turn = 0;
     const DropKey key = drop_key(a.drop);
     const float count = static_cast<float>(a.n);
-    float *pg = part_gamma + static_cast<int64_t>(blockIdx.x) * a.n;
-    float *pb = part_beta ? part_beta + static_cast<int64_t>(blockIdx.x) * a.n : nullptr;
+    float *pg = part_gamma + static_cast<int64_t>(blockIdx.x) * part_stride;
+    float *pb = part_beta ? part_beta + static_cast<int64_t>(blockIdx.x) * part_stride : nullptr;
     bool fresh = true;
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const int64_t e0 = r * a.n;
@@ -94,11 +95,12 @@ mrn_norm_backward_looped_kernel(const BackwardArgs a, float *part_gamma, float *
 template <class T, int K, bool EDGE, bool WARP, bool RMS>
 __global__ void __launch_bounds__(WARP ? 128 : tile_max_threads(K))
 mrn_norm_backward_tile_kernel(const BackwardArgs a, const TileArgs t, float *part_gamma,
-                              float *part_beta) {
+                              float *part_beta, const int64_t part_stride) {
     extern __shared__ __align__(16) unsigned char ring_bytes[];
     __shared__ RowSumSlots<2> slots;
+    __shared__ float stats[kTileMaxStages][2][128];   // mean and rstd of the ring's rows, per team
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(ring_bytes));
-    const RowTile<T, K, EDGE, WARP> tile(a.rows, a.n, t);
+    RowTile<T, K, EDGE, WARP> tile(a.rows, a.n, t);
     const int ops_count = a.dstream ? 3 : 2;
     const int64_t back = static_cast<int64_t>(t.mis) * T::kBytes;
     const char *const ops[kTileMaxOperands] = {
@@ -106,152 +108,167 @@ mrn_norm_backward_tile_kernel(const BackwardArgs a, const TileArgs t, float *par
         a.dstream ? static_cast<const char *>(a.dstream) - back : nullptr};
     char *const dx = static_cast<char *>(a.dx) - back;
     char *const dres = a.dres ? static_cast<char *>(a.dres) - back : nullptr;
-    uint32_t in[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) in[k] = tile.inside(k);
+    RingWalk walk(ops_count * K * tile.region, t.stages);
+    const int ahead = t.stages - 1;
+    tile.clear(ring, t.stages, ops_count);
     if (tile.cl > 1) cluster_arrive_relaxed();   // (peers' shared memory is written later)
     pdl_enter();
-    const int ahead = t.stages - 1;
-    for (int s = 0; s < ahead; ++s) {
-        const int64_t r = tile.row + s * tile.stride;
-        tile.issue(ring, s, r, r < a.rows, ops, ops_count);
-        cp_async_commit();
-    }
+    // mean and rstd travel with their row, so that no load of them is waited for
+    auto issue = [&](int to, int rows_ahead) {
+        const int64_t r = tile.row + rows_ahead * tile.stride;
+        if (!RMS && tile.leads && r < a.rows) {
+            cp_async4(static_cast<uint32_t>(__cvta_generic_to_shared(&stats[to][0][tile.team])), a.mean + r);
+            cp_async4(static_cast<uint32_t>(__cvta_generic_to_shared(&stats[to][1][tile.team])), a.rstd + r);
+        }
+        tile.issue(ring + to * walk.bytes, rows_ahead, ops, ops_count);
+    };
+    for (int s = 0; s < ahead; ++s) issue(s, s);
     const DropKey key = drop_key(a.drop);
     Slot<T> gamma[K];
-    tile.weights(gamma, in, a.gamma);
-    float sum_g[K][8], sum_b[K][8];
+    tile.weights(gamma, a.gamma);
+    uint64_t sum_g[K][4], sum_b[K][4];
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum_g[k][i] = sum_b[k][i] = 0.0f;
-    if (tile.cl > 1) cluster_wait_acquire();
+        for (int i = 0; i < 4; ++i) sum_g[k][i] = sum_b[k][i] = 0;
     const float inv_n = 1.0f / static_cast<float>(a.n);
-    int turn = 0, stage = 0, fill = ahead;
-    float mean = 0.0f, rstd = 0.0f;
-    if (!RMS && tile.row < a.rows) {
-        mean = a.mean[tile.row];
-        rstd = a.rstd[tile.row];
-    }
-    for (int64_t it = 0; tile.cta_row(it) < a.rows; ++it) {
-        const int64_t r = tile.row + it * tile.stride;
-        const bool ok = r < a.rows;
+    int turn = 0;
+    if (tile.cl > 1) cluster_wait_acquire();
+    for (; tile.cta_row() < a.rows; tile.advance(), walk.next()) {
         __syncwarp();
-        const int64_t next = r + ahead * tile.stride;
-        tile.issue(ring, fill, next, next < a.rows, ops, ops_count);
-        cp_async_commit();
-        fill = fill + 1 == t.stages ? 0 : fill + 1;
-        float next_mean = 0.0f, next_rstd = 0.0f;
-        if (!RMS && r + tile.stride < a.rows) {
-            next_mean = a.mean[r + tile.stride];
-            next_rstd = a.rstd[r + tile.stride];
-        }
+        issue(walk.write, ahead);
         cp_async_wait(ahead);
         __syncwarp();
+        const uint32_t from = ring + walk.read * walk.bytes;
         Slot<T> dy[K], x[K];
-        tile.fetch(dy, ring, stage, 0, ops_count);
-        tile.mask(dy, in);
-        tile.fetch(x, ring, stage, 1, ops_count);
-        tile.mask(x, in);
+        tile.fetch(dy, from, 0);
+        tile.fetch(x, from, 1);
+        const bool ok = !WARP || tile.row < a.rows;
+        const float mean = RMS || !ok ? 0.0f : stats[walk.read][0][tile.team];
+        float rstd = RMS || !ok ? 0.0f : stats[walk.read][1][tile.team];
+        // w = dy gamma and xh (RMSNorm: x) stay until the outputs.
         // LayerNorm: sums of w and w xh; RMSNorm: of x^2 and w x
-        float s[2] = {0.0f, 0.0f};
+        uint64_t w[K][4], xh[K][4];
+        uint64_t s0 = 0, s1 = 0;
+        const uint64_t minus = f2_pack(-mean, -mean);
+        uint64_t scale = f2_pack(rstd, rstd);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float d = dy[k].get(i);
-                const float w = d * gamma[k].get(i);
+            for (int i = 0; i < 4; ++i) {
+                const uint64_t d = dy[k].pair(i);
+                w[k][i] = f2_mul(d, gamma[k].pair(i));
                 if (RMS) {
-                    s[0] = fmaf(x[k].get(i), x[k].get(i), s[0]);
-                    s[1] = fmaf(w, x[k].get(i), s[1]);
+                    xh[k][i] = x[k].pair(i);
+                    s0 = f2_fma(xh[k][i], xh[k][i], s0);
                 } else {
-                    const float xh = (x[k].get(i) - mean) * rstd;
-                    s[0] += w;
-                    s[1] = fmaf(w, xh, s[1]);
-                    sum_g[k][i] = fmaf(d, xh, sum_g[k][i]);
-                    sum_b[k][i] += d;
+                    xh[k][i] = f2_mul(f2_add(x[k].pair(i), minus), scale);
+                    s0 = f2_add(s0, w[k][i]);
+                    sum_g[k][i] = f2_fma(d, xh[k][i], sum_g[k][i]);
+                    sum_b[k][i] = f2_add(sum_b[k][i], d);
                 }
+                s1 = f2_fma(w[k][i], xh[k][i], s1);
             }
         }
+        float s[2] = {f2_sum(s0), f2_sum(s1)};
         row_sum<2, WARP>(s, slots, turn, tile.width, tile.cl, tile.crank);
+        // ds = rstd w - rstd c1 - xh rstd c2
         float c1 = 0.0f, c2;
         if (RMS) {
-            rstd = 1.0f / sqrtf(s[0] * inv_n + a.eps);
-            c2 = s[1] * inv_n * rstd;
+            rstd = inv_sqrt(fmaf(s[0], inv_n, a.eps));
+            scale = f2_pack(rstd, rstd);
+            c2 = -(s[1] * inv_n * rstd) * rstd * rstd;
         } else {
-            c1 = s[0] * inv_n;
-            c2 = s[1] * inv_n;
+            c1 = -(s[0] * inv_n) * rstd;
+            c2 = -(s[1] * inv_n) * rstd;
         }
-        Slot<T> ds[K];
-        if (a.dstream) tile.fetch(ds, ring, stage, 2, ops_count);
-        stage = stage + 1 == t.stages ? 0 : stage + 1;
+        const uint64_t c1p = f2_pack(c1, c1), c2p = f2_pack(c2, c2);
+        if (a.dstream) tile.fetch(x, from, 2);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            float o[8];
+            uint64_t o[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float d = dy[k].get(i);
-                const float xh = RMS ? x[k].get(i) * rstd : (x[k].get(i) - mean) * rstd;
-                o[i] = fmaf(-xh, c2, fmaf(d, gamma[k].get(i), -c1)) * rstd;
-                if (RMS && ok) sum_g[k][i] = fmaf(d, xh, sum_g[k][i]);
+            for (int i = 0; i < 4; ++i) {
+                o[i] = f2_fma(xh[k][i], c2p, RMS ? f2_mul(w[k][i], scale)
+                                                 : f2_fma(w[k][i], scale, c1p));
+                if (RMS) sum_g[k][i] = f2_fma(dy[k].pair(i), f2_mul(xh[k][i], scale), sum_g[k][i]);
             }
             if (a.dstream) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] += ds[k].get(i);
+                for (int i = 0; i < 4; ++i) o[i] = f2_add(o[i], x[k].pair(i));
             }
             if (!ok) continue;
             Slot<T> out;
-            out.put(o);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) out.put_pair(i, o[i]);
             if (a.dres) {
-                tile.store(dres, r, k, in[k], out);
-                if (in[k] != 0u) {
-                    uint32_t w[4] = {0u, 0u, 0u, 0u};
-                    if (a.drop.threshold != 0u)
-                        philox_lanes(key, static_cast<uint64_t>((tile.slot0(r) >> 3) + tile.first +
-                                                                k * tile.width), w);
+                tile.store(dres, k, out);
+                if (tile.in[k] != 0u) {
+                    const DropGroup g = drop_group(key, tile.group(k), a.drop.threshold);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        o[i] = drop_scale(o[i], drop_keeps(w, i, a.drop.threshold), a.drop.scale);
-                    out.put(o);
-                }
-            }
-            tile.store(dx, r, k, in[k], out);
-        }
-        mean = next_mean;
-        rstd = next_rstd;
-    }
-    cp_async_wait(0);
-    __syncthreads();   // the ring is free: the CTA's column sums go through it
-    float *const buf = reinterpret_cast<float *>(ring_bytes);
-    const int64_t part = (WARP ? blockIdx.x : blockIdx.x / tile.cl) * a.n;
-    const int lo = WARP ? 0 : static_cast<int>(tile.crank) * K * static_cast<int>(blockDim.x) * 8 - tile.off;
-    const int span = K * tile.width * 8;      // columns lo .. lo + span of this CTA
-    const int turns = WARP ? static_cast<int>(blockDim.x) / tile.width : 1;
-    const int mine = WARP ? static_cast<int>(threadIdx.x) / tile.width : 0;
-    for (int which = 0; which < (!RMS && part_beta ? 2 : 1); ++which) {
-        float *const out = which == 0 ? part_gamma : part_beta;
-        for (int g = 0; g < turns; ++g) {
-            if (g == mine) {
-#pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    // (WARP: rows of one CTA may start at different offsets, so columns
-                    // are counted from the row's first)
-                    const int at = tile.column(k) - lo;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if (!((in[k] >> i) & 1u)) continue;
-                        const float v = which == 0 ? sum_g[k][i] : sum_b[k][i];
-                        buf[at + i] = g == 0 ? v : buf[at + i] + v;
+                    for (int i = 0; i < 4; ++i) {
+                        float lo, hi;
+                        f2_unpack(o[i], lo, hi);
+                        out.put_pair(i, f2_pack(drop_scale(lo, g.keeps(2 * i), a.drop.scale),
+                                                drop_scale(hi, g.keeps(2 * i + 1), a.drop.scale)));
                     }
                 }
             }
+            tile.store(dx, k, out);
+        }
+    }
+    cp_async_wait(0);
+    if constexpr (!WARP) {
+        // one partial row per CTA (or cluster), in slots: the join knows the row's offset
+        const int64_t part = blockIdx.x / tile.cl;
+#pragma unroll
+        for (int which = 0; which < (RMS ? 1 : 2); ++which) {
+            if (which == 1 && !part_beta) break;
+            float *const out = (which == 0 ? part_gamma : part_beta) + part * part_stride;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                if (tile.in[k] == 0u) continue;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    Frag<F32, 4> v;
+                    float f[4];
+                    f2_unpack(which == 0 ? sum_g[k][2 * i] : sum_b[k][2 * i], f[0], f[1]);
+                    f2_unpack(which == 0 ? sum_g[k][2 * i + 1] : sum_b[k][2 * i + 1], f[2], f[3]);
+                    v.put(f);
+                    st_global(out + (tile.first + k * tile.width) * 8 + 4 * i, v);
+                }
+            }
+        }
+    } else {
+        // the rows' sums of this CTA through the ring, in slots; then one column per thread,
+        // over the rows in order
+        const int span = K * tile.width * 8;
+        const int teams = static_cast<int>(blockDim.x) / tile.width;
+        const int64_t row0 = static_cast<int64_t>(blockIdx.x) * teams;
+        float *const buf = reinterpret_cast<float *>(ring_bytes);
+#pragma unroll
+        for (int which = 0; which < (RMS ? 1 : 2); ++which) {
+            if (which == 1 && !part_beta) break;
             __syncthreads();
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                uint64_t *to = reinterpret_cast<uint64_t *>(buf + tile.team * span +
+                                                            (tile.first + k * tile.width) * 8);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) to[i] = which == 0 ? sum_g[k][i] : sum_b[k][i];
+            }
+            __syncthreads();
+            float *const out = (which == 0 ? part_gamma : part_beta) +
+                               static_cast<int64_t>(blockIdx.x) * part_stride;
+            for (int j = threadIdx.x; j < static_cast<int>(a.n); j += blockDim.x) {
+                float v = 0.0f;
+                for (int g = 0; g < teams; ++g) {
+                    const int off = EDGE ? static_cast<int>((t.mis + (row0 + g) * a.n) & 7) : 0;
+                    v += buf[g * span + j + off];
+                }
+                out[j] = v;
+            }
         }
-        for (int j = threadIdx.x; j < span; j += blockDim.x) {
-            const int64_t col = static_cast<int64_t>(lo) + j;
-            if (col >= 0 && col < a.n) out[part + col] = buf[j];
-        }
-        __syncthreads();
     }
 }
 
@@ -262,7 +279,7 @@ cudaError_t launch_backward_tile(const BackwardArgs &a, const TilePlan &p, float
     const TileArgs t = {p.lanes, p.stages, p.mis};
     const int64_t shared = tile_ring_bytes(T::kBytes, K, p.threads, p.stages, a.dstream ? 3 : 2);
     return launch_tile(cache, mrn_norm_backward_tile_kernel<T, K, EDGE, WARP, RMS>, p, shared, pdl,
-                       stream, launches, a, t, pg, pb);
+                       stream, launches, a, t, pg, pb, part_stride_of(a.n));
 }
 
 template <class T, int K, bool WARP>
@@ -275,42 +292,55 @@ cudaError_t launch_backward_k(const BackwardArgs &a, const TilePlan &p, float *p
                   : launch_backward_tile<T, K, false, WARP, false>(a, p, pg, pb, pdl, stream, launches);
 }
 
-// dgamma (blockIdx.y == 0) and dbeta (1): the sum of `parts` partial rows.  A
-// CTA owns 32 columns; its 32 warps take every 32nd partial row each and are
-// joined in shared memory, in order.
+// dgamma (blockIdx.y == 0) and dbeta (1): the sum of `parts` partial rows.  A CTA owns 32
+// columns; its 32 warps take every 32nd partial row each, eight loads in flight, and are
+// joined in shared memory, in order.  shifted: partial row p starts as row p of the matrix
+// does, (mis + p n) mod 8 elements into its first slot.
 constexpr int kJoinColumns = 32;
 constexpr int kJoinThreads = 1024;
+constexpr int kJoinFlight = 8;
 
-__global__ void __launch_bounds__(kJoinThreads)
-mrn_norm_backward_join_kernel(const float *part_gamma, const float *part_beta, float *dgamma,
-                              float *dbeta, int64_t parts, int64_t n) {
+struct JoinArgs {
+    const float *part_gamma, *part_beta;
+    float *dgamma, *dbeta;
+    int64_t parts, n, stride;
+    int mis;
+    bool shifted;
+};
+
+__global__ void __launch_bounds__(kJoinThreads) mrn_norm_backward_join_kernel(const JoinArgs a) {
     __shared__ float sums[32][kJoinColumns + 1];
     pdl_enter();
-    const float *part = blockIdx.y == 0 ? part_gamma : part_beta;
-    float *out = blockIdx.y == 0 ? dgamma : dbeta;
+    const float *part = blockIdx.y == 0 ? a.part_gamma : a.part_beta;
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;
     const int64_t j = static_cast<int64_t>(blockIdx.x) * kJoinColumns + lane;
     float s = 0.0f;
-    if (j < n) {
-        for (int64_t p = warp; p < parts; p += 32) s += part[p * n + j];
+    for (int64_t p0 = warp; p0 < a.parts; p0 += 32 * kJoinFlight) {
+        float v[kJoinFlight];
+#pragma unroll
+        for (int i = 0; i < kJoinFlight; ++i) {
+            const int64_t p = p0 + 32 * i;
+            const int64_t off = a.shifted ? (a.mis + p * a.n) & 7 : 0;
+            v[i] = p < a.parts && j < a.n ? part[p * a.stride + off + j] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < kJoinFlight; ++i) s += v[i];
     }
     sums[warp][lane] = s;
     __syncthreads();
     // warp c adds up column c: lane w holds warp w's sum
     const float t = warp_allsum(sums[lane][warp]);
     const int64_t jc = static_cast<int64_t>(blockIdx.x) * kJoinColumns + warp;
-    if (lane == 0 && jc < n) out[jc] = t;
+    if (lane == 0 && jc < a.n) (blockIdx.y == 0 ? a.dgamma : a.dbeta)[jc] = t;
 }
 
-cudaError_t launch_join(const float *pg, const float *pb, float *dgamma, float *dbeta,
-                        int64_t parts, int64_t n, bool pdl, cudaStream_t stream,
-                        uint64_t *launches) {
-    const int64_t ctas = (n + kJoinColumns - 1) / kJoinColumns;
+cudaError_t launch_join(const JoinArgs &a, bool pdl, cudaStream_t stream, uint64_t *launches) {
+    const int64_t ctas = (a.n + kJoinColumns - 1) / kJoinColumns;
     if (ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas), dbeta ? 2 : 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas), a.dbeta ? 2 : 1, 1);
     cfg.blockDim = dim3(kJoinThreads, 1, 1);
     cfg.stream = stream;
     if (pdl) {
@@ -319,8 +349,7 @@ cudaError_t launch_join(const float *pg, const float *pb, float *dgamma, float *
         cfg.attrs = attr;
         cfg.numAttrs = 1;
     }
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, mrn_norm_backward_join_kernel, pg, pb, dgamma,
-                                               dbeta, parts, n);
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, mrn_norm_backward_join_kernel, a);
     if (err == cudaSuccess) ++*launches;
     return err;
 }
@@ -329,34 +358,46 @@ template <class T>
 cudaError_t launch_backward_typed(const BackwardArgs &a, int sms, bool pdl, cudaStream_t stream,
                                   uint64_t *launches) {
     const int64_t most = backward_parts(a.rows, a.n, sms);
-    if (most == 0) return launch_join(nullptr, nullptr, a.dgamma, a.dbeta, 0, a.n, pdl, stream, launches);
+    JoinArgs join = {};
+    join.dgamma = a.dgamma;
+    join.dbeta = a.dbeta;
+    join.n = a.n;
+    join.stride = part_stride_of(a.n);
+    if (most == 0) return launch_join(join, pdl, stream, launches);
     const int mis = common_offset(T::kBytes, a.dy, a.x, a.dstream, static_cast<const void *>(a.dx),
                                   static_cast<const void *>(a.dres));
     TilePlan p = {};
     // (a generator group is a slot only when the operands start on a slot boundary)
     if (mis == 0 || (mis > 0 && a.drop.threshold == 0)) {
-        const TileWish wish = {a.dstream ? 3 : 2, 512, kPartsPerSm};
+        const TileWish wish = {a.dstream ? 3 : 2, 2, 512, kPartsPerSm};
         p = plan_tiles(a.rows, a.n, T::kBytes, mis, wish, sms);
     }
     const int64_t parts = p.ok ? p.ctas / p.cluster : most;
     if (parts > most) return cudaErrorInvalidConfiguration;   // (the workspace holds `most`)
     float *pg = a.workspace;
-    float *pb = a.dbeta ? a.workspace + parts * a.n : nullptr;
+    float *pb = a.dbeta ? a.workspace + parts * join.stride : nullptr;
     cudaError_t err;
     if (p.ok && p.warp) {
         err = p.k == 1   ? launch_backward_k<T, 1, true>(a, p, pg, pb, pdl, stream, launches)
               : p.k == 2 ? launch_backward_k<T, 2, true>(a, p, pg, pb, pdl, stream, launches)
                          : launch_backward_k<T, 4, true>(a, p, pg, pb, pdl, stream, launches);
     } else if (p.ok) {
-        err = p.k == 1 ? launch_backward_k<T, 1, false>(a, p, pg, pb, pdl, stream, launches)
-                       : launch_backward_k<T, 2, false>(a, p, pg, pb, pdl, stream, launches);
+        err = p.k == 1   ? launch_backward_k<T, 1, false>(a, p, pg, pb, pdl, stream, launches)
+              : p.k == 2 ? launch_backward_k<T, 2, false>(a, p, pg, pb, pdl, stream, launches)
+              : p.k == 3 ? launch_backward_k<T, 3, false>(a, p, pg, pb, pdl, stream, launches)
+                         : launch_backward_k<T, 4, false>(a, p, pg, pb, pdl, stream, launches);
     } else {
         const auto fn = a.rms ? mrn_norm_backward_looped_kernel<T, true>
                               : mrn_norm_backward_looped_kernel<T, false>;
-        err = launch_plain(fn, parts, kLoopedThreads, 0, pdl, stream, launches, a, pg, pb);
+        err = launch_plain(fn, parts, kLoopedThreads, 0, pdl, stream, launches, a, pg, pb, join.stride);
     }
     if (err != cudaSuccess) return err;
-    return launch_join(pg, pb, a.dgamma, a.dbeta, parts, a.n, pdl, stream, launches);
+    join.part_gamma = pg;
+    join.part_beta = pb;
+    join.parts = parts;
+    join.mis = p.mis;
+    join.shifted = p.ok && p.edge && !p.warp;
+    return launch_join(join, pdl, stream, launches);
 }
 
 cudaError_t launch_norm_backward(bool bf16, const BackwardArgs &a, int sms, bool pdl,

@@ -28,13 +28,16 @@ struct TileArgs {
 };
 
 constexpr int kTileMaxThreads = 512;
-constexpr int tile_max_threads(int k) { return k >= 4 ? 256 : kTileMaxThreads; }
+constexpr int tile_max_threads(int k) { return k >= 3 ? 256 : kTileMaxThreads; }
+constexpr int kTileMaxStages = 4;
 constexpr int kTileMaxOperands = 3;
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool ok) {
-    const int bytes = ok ? 16 : 0;   // 0: the 16 bytes are filled with zeros, src is not read
-    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;"
-                 :: "r"(dst), "l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;"
+                 :: "r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -94,158 +97,213 @@ template <class T, int K, bool EDGE, bool WARP> struct RowTile {
     static constexpr int kChunks = T::kBytes / 2;          // 16-byte chunks per slot
     static constexpr int kChunkElems = 8 / kChunks;
 
-    int width;          // threads per row (in this CTA)
-    int first;          // this thread's first slot; slot k is first + k * width
-    int off;            // elements of the row's first slot that precede the row
-    int64_t n;
-    int64_t row;        // this thread's row; the next is row + stride
-    int64_t stride;
-    int64_t rows;
-    int mis;
-    uint32_t lane_base;   // shared-memory offset of this thread's chunk 0 in a ring region
-    uint32_t slot_base;   // ... of this thread's slot
-    int chunk0;           // first chunk this thread copies, in elements of the slot row
-    int group_lanes;      // lanes that copy together
+    int width;            // threads per row (in this CTA)
+    int first;            // this thread's first slot; slot k is first + k * width
+    int off;              // elements of the row's first slot that precede the row
     unsigned cl, crank;
+    int64_t n, rows;
+    int64_t row;          // this thread's row; the next is row + stride
+    int64_t stride;
+    int64_t at;           // byte offset of the row's slot 0 from the slot boundary below its operand
+    int64_t step;         // bytes to the next row's
+    int team;             // index in the CTA of the lanes that copy together
+    bool leads;           // the first of them
+    uint32_t in[K];       // elements of slot k inside the row: bit i for element i
+    uint32_t copies;      // chunks this thread copies: bit k * kChunks + c
+    uint32_t region;      // bytes of one slot index k of all threads in the ring
+    uint32_t copy_base;   // this thread's place in a region: as copier,
+    uint32_t slot_base;   // ... and as owner
+    int copy_off;         // byte offset in the row of the first chunk this thread copies
+    int copy_step;        // ... and from chunk to chunk of a slot
 
     __device__ __forceinline__ RowTile(int64_t rows_, int64_t n_, const TileArgs &t)
-        : n(n_), rows(rows_), mis(t.mis) {
+        : n(n_), rows(rows_) {
         const int tid = threadIdx.x, lane = tid & 31;
+        int lanes = 32, li = lane;      // lanes that copy together, and this one's index
+        team = tid >> 5;
         if constexpr (WARP) {
             cl = 1;
             crank = 0;
             width = t.lanes;
-            group_lanes = t.lanes;
             first = tid & (t.lanes - 1);
             const int rows_per_cta = blockDim.x / t.lanes;
             row = static_cast<int64_t>(blockIdx.x) * rows_per_cta + tid / t.lanes;
             stride = static_cast<int64_t>(gridDim.x) * rows_per_cta;
+            lanes = t.lanes;
+            li = first;
+            team = tid / t.lanes;
         } else {
             cl = cluster_nctarank();
             crank = cluster_ctarank();
             width = blockDim.x;
-            group_lanes = 32;
             first = tid + static_cast<int>(crank) * K * static_cast<int>(blockDim.x);
             row = blockIdx.x / cl;
             stride = gridDim.x / cl;
         }
-        off = EDGE ? static_cast<int>((mis + row * n) & 7) : 0;
-        const int li = WARP ? first : lane;
-        const int head = first - li;               // slot of lane 0 of the lanes that copy together
-        chunk0 = head * 8 + li * kChunkElems;
-        lane_base = static_cast<uint32_t>(((tid - li) * kChunks + li) * 16);
+        leads = li == 0;
+        const int64_t e0 = t.mis + row * n;
+        off = EDGE ? static_cast<int>(e0 & 7) : 0;
+        at = (e0 - off) * T::kBytes;
+        step = stride * n * T::kBytes;
+        region = blockDim.x * kChunks * 16;
+        const int chunk0 = (first - li) * 8 + li * kChunkElems;     // element in the slot row
+        copy_off = chunk0 * T::kBytes;
+        copy_step = lanes * 16;
+        copy_base = static_cast<uint32_t>(((tid - li) * kChunks + li) * 16);
         slot_base = static_cast<uint32_t>(tid * kChunks * 16);
+        copies = 0u;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int64_t j = column(k);
+            uint32_t m = 0xFFu;
+            if (j < 0) m &= 0xFFu << static_cast<int>(-j);
+            if (j + 8 > n) m = j < n ? m & (0xFFu >> static_cast<int>(j + 8 - n)) : 0u;
+            in[k] = m;
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+                const int64_t jc = chunk0 + k * width * 8 + c * lanes * kChunkElems - off;
+                if (jc < n && jc + kChunkElems > 0) copies |= 1u << (k * kChunks + c);
+            }
+        }
     }
 
     // First row of this CTA's iteration: uniform over the CTA, so that all its threads
     // make the same number of iterations.
-    __device__ __forceinline__ int64_t cta_row(int64_t it) const {
+    __device__ __forceinline__ int64_t cta_row() const {
         if constexpr (WARP) {
-            return (it * gridDim.x + blockIdx.x) * (blockDim.x / width);
+            return row - team;
         } else {
-            return row + it * stride;
+            return row;
         }
     }
     __device__ __forceinline__ int column(int k) const { return (first + k * width) * 8 - off; }
-    // Elements of slot k inside the row: bit i for element i.
-    __device__ __forceinline__ uint32_t inside(int k) const {
-        const int64_t j = column(k);
-        if (j >= n || j + 8 <= 0) return 0u;
-        uint32_t m = 0xFFu;
-        if (j < 0) m &= 0xFFu << static_cast<int>(-j);
-        if (j + 8 > n) m &= 0xFFu >> static_cast<int>(j + 8 - n);
-        return m;
-    }
-    // Element index (in the flattened matrix, counted from the slot boundary below its
-    // base) of row r's slot 0.
-    __device__ __forceinline__ int64_t slot0(int64_t r) const { return (mis + r * n) & ~int64_t(7); }
 
-    // Copies row r of `count` operands into ring stage `stage`.
-    __device__ __forceinline__ void issue(uint32_t ring, int stage, int64_t r, bool ok,
-                                          const char *const (&ops)[kTileMaxOperands], int count) const {
-        const uint32_t region = blockDim.x * kChunks * 16;
-        const int64_t base = ok ? slot0(r) : 0;
+    // Zeroes a ring of `stages` stages of `count` operands: the chunks outside the row are
+    // never copied, and read as zeros ever after.
+    __device__ __forceinline__ void clear(uint32_t ring, int stages, int count) const {
+        for (int i = 0; i < stages * count * K; ++i) {
 #pragma unroll
-        for (int o = 0; o < kTileMaxOperands; ++o) {
-            if (o >= count) break;
-            const char *src = ops[o] + base * T::kBytes;
-            const uint32_t dst = ring + ((stage * count + o) * K) * region + lane_base;
+            for (int c = 0; c < kChunks; ++c)
+                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};"
+                             :: "r"(ring + i * region + copy_base + c * copy_step), "r"(0u) : "memory");
+        }
+        __syncwarp();
+    }
+    // Copies the row `ahead` rows from this one into the ring's stage at `to` (one group of
+    // asynchronous copies with what was issued since the last).
+    __device__ __forceinline__ void issue(uint32_t to, int ahead, const char *const (&ops)[kTileMaxOperands],
+                                          int count) const {
+        if (row + ahead * stride < rows) {
+            const int64_t from = at + ahead * step + copy_off;
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
+            for (int o = 0; o < kTileMaxOperands; ++o) {
+                if (o >= count) break;
+                const char *src = ops[o] + from;
+                const uint32_t dst = to + o * K * region + copy_base;
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c) {
-                    const int e = chunk0 + k * width * 8 + c * group_lanes * kChunkElems;
-                    const int64_t j = e - off;
-                    const bool in = ok && j < n && (!EDGE || j + kChunkElems > 0);
-                    cp_async16(dst + k * region + c * group_lanes * 16,
-                               in ? src + static_cast<int64_t>(e) * T::kBytes : ops[o], in);
+                for (int k = 0; k < K; ++k) {
+#pragma unroll
+                    for (int c = 0; c < kChunks; ++c) {
+                        if ((copies >> (k * kChunks + c)) & 1u)
+                            cp_async16(dst + k * region + c * copy_step,
+                                       src + k * (width * 8 * T::kBytes) + c * copy_step);
+                    }
+                }
+            }
+        }
+        cp_async_commit();
+    }
+    // This thread's slots of operand o in the stage at `from`, zero outside the row.
+    __device__ __forceinline__ void fetch(Slot<T> (&s)[K], uint32_t from, int o) const {
+        const uint32_t src = from + o * K * region + slot_base;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            ld_shared_slot(s[k], src + k * region);
+            if constexpr (EDGE) {
+                if (in[k] != 0xFFu && in[k] != 0u) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (!((in[k] >> i) & 1u)) s[k].clear(i);
+                }
+            }
+        }
+        if constexpr (WARP) {
+            if (row >= rows) {      // (past the last row: the stage holds an earlier one)
+#pragma unroll
+                for (int k = 0; k < K; ++k) s[k].zero();
+            }
+        }
+    }
+    // Stores slot k of this row (the elements inside it) at `base`, the slot boundary below
+    // the operand's first element.
+    __device__ __forceinline__ void store(char *base, int k, const Slot<T> &s) const {
+        char *p = base + at + (first + k * width) * (8 * T::kBytes);
+        if (!EDGE || in[k] == 0xFFu) {
+            if (in[k] != 0u) st_slot(p, s);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if ((in[k] >> i) & 1u) s.st_one(p + i * T::kBytes, i);
+        }
+    }
+    // Generator group of slot k (the operands start on a slot boundary).
+    __device__ __forceinline__ uint64_t group(int k) const {
+        return static_cast<uint64_t>(at) / (8 * T::kBytes) + static_cast<uint64_t>(first + k * width);
+    }
+    // The thread's columns of a weight vector, zeros outside the row; once per CTA.  All
+    // loads are independent of each other.
+    __device__ __forceinline__ void weights(Slot<T> (&s)[K], const void *w) const {
+        const bool whole = !EDGE && reinterpret_cast<uintptr_t>(w) % 16 == 0;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int64_t j = column(k);
+            if (whole) {
+                const int64_t jj = in[k] ? j : 0;
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c)
+                    asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(s[k].w[4 * c]), "=r"(s[k].w[4 * c + 1]),
+                                   "=r"(s[k].w[4 * c + 2]), "=r"(s[k].w[4 * c + 3])
+                                 : "l"(elem_ptr<T>(w, jj) + c * 16));
+                if (!in[k]) s[k].zero();
+            } else {
+                Frag<T, 1> f[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ld_ro(f[i], elem_ptr<T>(w, ((in[k] >> i) & 1u) ? j + i : 0));
+                s[k].zero();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if constexpr (T::kBytes == 4) {
+                        s[k].w[i] = ((in[k] >> i) & 1u) ? f[i].w : 0u;
+                    } else {
+                        if ((in[k] >> i) & 1u)
+                            s[k].w[i >> 1] |= static_cast<uint32_t>(f[i].h) << ((i & 1) * 16);
+                    }
                 }
             }
         }
     }
-    __device__ __forceinline__ void fetch(Slot<T> (&s)[K], uint32_t ring, int stage, int o,
-                                          int count) const {
-        const uint32_t region = blockDim.x * kChunks * 16;
-        const uint32_t src = ring + ((stage * count + o) * K) * region + slot_base;
-#pragma unroll
-        for (int k = 0; k < K; ++k) ld_shared_slot(s[k], src + k * region);
+    __device__ __forceinline__ void advance() {
+        row += stride;
+        at += step;
     }
-    // Zeroes the elements of the slots that lie outside the row (other rows' values).
-    __device__ __forceinline__ void mask(Slot<T> (&s)[K], const uint32_t (&in)[K]) const {
-        if constexpr (EDGE) {
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                if (in[k] == 0xFFu || in[k] == 0u) continue;   // (0: filled with zeros)
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (!((in[k] >> i) & 1u)) s[k].clear(i);
-            }
-        }
-    }
-    // Stores slot k of row r (the elements inside it) at `base`, the slot boundary below the
-    // operand's first element.
-    __device__ __forceinline__ void store(char *base, int64_t r, int k, uint32_t in,
-                                          const Slot<T> &s) const {
-        char *p = base + (slot0(r) + static_cast<int64_t>(first + k * width) * 8) * T::kBytes;
-        if (!EDGE || in == 0xFFu) {
-            if (in != 0u) st_slot(p, s);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if ((in >> i) & 1u) s.st_one(p + i * T::kBytes, i);
-        }
-    }
-    // The thread's columns of a weight vector (zeros outside the row), element by element:
-    // once per CTA.
-    __device__ __forceinline__ void weights(Slot<T> (&s)[K], const uint32_t (&in)[K],
-                                            const void *w) const {
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int64_t j = column(k);
-            s[k].zero();
-            if constexpr (T::kBytes == 4) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if ((in[k] >> i) & 1u) {
-                        Frag<T, 1> f;
-                        ld_ro(f, elem_ptr<T>(w, j + i));
-                        s[k].w[i] = f.w;
-                    }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if ((in[k] >> i) & 1u) {
-                        Frag<T, 1> f;
-                        ld_ro(f, elem_ptr<T>(w, j + i));
-                        s[k].w[i >> 1] |= static_cast<uint32_t>(f.h) << ((i & 1) * 16);
-                    }
-            }
-        }
+};
+
+// The ring's stages: the one the current row is read from and the one that the row `stages - 1`
+// rows on is copied to.
+struct RingWalk {
+    uint32_t bytes;
+    int stages, read, write;
+    __device__ __forceinline__ RingWalk(uint32_t stage_bytes, int stages_)
+        : bytes(stage_bytes), stages(stages_), read(0), write(stages_ - 1) {}
+    __device__ __forceinline__ void next() {
+        read = read + 1 == stages ? 0 : read + 1;
+        write = write + 1 == stages ? 0 : write + 1;
     }
 };
 
 // Dynamic shared memory that a ring may use: the rest is the static row-sum slots.
-constexpr int64_t kTileSharedBudget = kSharedBytesPerCta - 4096;
+constexpr int64_t kTileSharedBudget = kSharedBytesPerCta - 8192;
 
 // Dynamic shared memory of a ring.
 inline int64_t tile_ring_bytes(int elem_bytes, int k, int threads, int stages, int operands) {
@@ -264,6 +322,7 @@ struct TilePlan {
 
 struct TileWish {
     int operands;          // row operands copied ahead
+    int slots_per_thread;  // for rows of a CTA
     int threads_per_sm;    // resident threads to aim for
     int most_ctas_per_sm;
 };
@@ -282,8 +341,9 @@ inline TilePlan plan_tiles(int64_t rows, int64_t n, int elem_bytes, int mis, con
         while (p.lanes * p.k < slots) p.lanes *= 2;
         p.threads = 128;
     } else {
-        p.k = slots <= 256 ? 1 : 2;
-        p.cluster = static_cast<int>((slots + 1023) / 1024);
+        p.k = wish.slots_per_thread;
+        const int64_t most = int64_t(p.k) * tile_max_threads(p.k);
+        p.cluster = static_cast<int>((slots + most - 1) / most);
         if (p.cluster > kMaxCluster) return p;
         const int64_t per = (slots + p.cluster - 1) / p.cluster;
         p.threads = static_cast<int>((per + 32 * p.k - 1) / (32 * p.k)) * 32;
@@ -292,10 +352,11 @@ inline TilePlan plan_tiles(int64_t rows, int64_t n, int elem_bytes, int mis, con
     int64_t per_sm = wish.threads_per_sm / p.threads;
     if (per_sm > wish.most_ctas_per_sm) per_sm = wish.most_ctas_per_sm;
     if (per_sm < 1) per_sm = 1;
-    const int64_t budget = (kTileSharedBudget - (per_sm - 1) * 4096) / per_sm;
+    const int64_t budget = (kTileSharedBudget - (per_sm - 1) * 8192) / per_sm;
     p.stages = static_cast<int>(budget / stage);
-    if (p.stages > 4) p.stages = 4;
+    if (p.stages > kTileMaxStages) p.stages = kTileMaxStages;
     if (p.stages < 1) return p;
+    //TUNE
     const int64_t rows_per_cta = p.warp ? p.threads / p.lanes : 1;
     int64_t groups = sms * per_sm / p.cluster;      // CTAs or clusters
     if (groups * rows_per_cta % 8 != 0 && groups > 8) groups -= groups % 8;

@@ -67,7 +67,10 @@ cudaError_t launch_dropout(bool bf16, const DropoutArgs &a, bool pdl, cudaStream
                            uint64_t *launches);
 
 // Partial sums of dgamma (and of dbeta) that a backward pass keeps at most: the
-// rows of [parts x n] floats in its workspace, for each of the two.
+// rows of [parts x part_stride_of(n)] floats in its workspace, for each of the two.
 int64_t backward_parts(int64_t rows, int64_t n, int sms);
+// Floats from one partial row to the next: whole slots of eight for a row that may
+// start anywhere in one.
+constexpr int64_t part_stride_of(int64_t n) { return (n + 14) / 8 * 8; }
 
 }  // namespace mrn

@@ -68,8 +68,9 @@ mrn_status drop_args(double p, const uint64_t *rng, uint64_t site, DropArgs *d) 
 mrn_status workspace_bytes_needed(int64_t rows, int64_t n, int64_t *bytes) {
     if (n < 1 || rows < 0 || n > INT64_MAX / 16) return MRN_ERR_INVALID_SIZE;
     const int64_t parts = backward_parts(rows, n, sm_count_of_current_device());
-    if (parts > 0 && n > INT64_MAX / 16 / parts) return MRN_ERR_INVALID_SIZE;
-    *bytes = 2 * parts * n * static_cast<int64_t>(sizeof(float));
+    const int64_t stride = part_stride_of(n);
+    if (parts > 0 && stride > INT64_MAX / 16 / parts) return MRN_ERR_INVALID_SIZE;
+    *bytes = 2 * parts * stride * static_cast<int64_t>(sizeof(float));
     return MRN_OK;
 }
 

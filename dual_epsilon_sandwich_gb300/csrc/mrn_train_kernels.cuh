@@ -56,22 +56,42 @@ __device__ __forceinline__ void philox_lanes(const DropKey &key, uint64_t group,
     w[3] = c3;
 }
 
-// Whether lane i (0..7) of a group is kept.
-__device__ __forceinline__ bool drop_keeps(const uint32_t (&w)[4], int i, uint32_t threshold) {
-    const uint32_t u = (i & 1) ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu;
-    return u >= threshold;
+// One group's lanes and the word threshold they are compared with: element i is kept when
+// its lane, moved to the upper half of a word, is >= at (the lower half left below an upper
+// lane does not change the comparison).  All kept (threshold 0) and all dropped (65536) need
+// no generator.
+struct DropGroup {
+    uint32_t w[4];
+    uint32_t at;
+    __device__ __forceinline__ bool keeps(int i) const {
+        return ((i & 1) ? w[i >> 1] : w[i >> 1] << 16) >= at;
+    }
+};
+
+__device__ __forceinline__ DropGroup drop_group(const DropKey &key, uint64_t group,
+                                                uint32_t threshold) {
+    DropGroup g;
+    g.w[0] = g.w[1] = g.w[2] = g.w[3] = 0u;
+    g.at = threshold == 0u ? 0u : 1u;
+    if (threshold != 0u && threshold < 65536u) {
+        philox_lanes(key, group, g.w);
+        g.at = threshold << 16;
+    }
+    return g;
 }
 
 // One element on its own.
 __device__ __forceinline__ bool drop_keeps_element(const DropKey &key, int64_t e,
                                                    uint32_t threshold) {
-    if (threshold == 0u) return true;
-    uint32_t w[4];
-    philox_lanes(key, static_cast<uint64_t>(e) >> 3, w);
+    const DropGroup g = drop_group(key, static_cast<uint64_t>(e) >> 3, threshold);
     const int i = static_cast<int>(e & 7);
-    const uint32_t word = i < 4 ? (i < 2 ? w[0] : w[1]) : (i < 6 ? w[2] : w[3]);
-    return ((i & 1) ? word >> 16 : word & 0xFFFFu) >= threshold;
+    const uint32_t word = i < 4 ? (i < 2 ? g.w[0] : g.w[1]) : (i < 6 ? g.w[2] : g.w[3]);
+    return ((i & 1) ? word : word << 16) >= g.at;
 }
+
+// 1 / sqrt(v): within 2 units in the last place (rsqrtf), and 0 at infinity.  The IEEE
+// square root and division would cost each thread of a row some forty instructions more.
+__device__ __forceinline__ float inv_sqrt(float v) { return rsqrtf(v); }
 
 // dropout(v).
 __device__ __forceinline__ float drop_scale(float v, bool keep, float scale) {
@@ -92,20 +112,35 @@ template <int N> struct CtaSumSlots {
     float v[2][N][32];
 };
 
-template <int N>
-__device__ __forceinline__ void cta_sum(float (&v)[N], CtaSumSlots<N> &s, int &turn) {
+__device__ __forceinline__ void cta_sum(float (&v)[1], CtaSumSlots<1> &s, int &turn) {
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;
     const int nwarps = blockDim.x >> 5;
     turn ^= 1;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        v[i] = warp_allsum(v[i]);
-        if (lane == 0) s.v[turn][i][warp] = v[i];
-    }
+    v[0] = warp_allsum(v[0]);
+    if (lane == 0) s.v[turn][0][warp] = v[0];
     __syncthreads();
+    v[0] = warp_allsum(lane < nwarps ? s.v[turn][0][lane] : 0.0f);
+}
+
+// Two values at once (at most 16 warps): the first exchange leaves one value with each half
+// of the warp, so that both take little more than the shuffles of one.
+__device__ __forceinline__ void cta_sum(float (&v)[2], CtaSumSlots<2> &s, int &turn) {
+    const int lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5;
+    const int nwarps = blockDim.x >> 5;
+    const int half = lane >> 4;
+    turn ^= 1;
+    float t = (half ? v[1] : v[0]) + __shfl_xor_sync(0xFFFFFFFFu, half ? v[0] : v[1], 16);
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = warp_allsum(lane < nwarps ? s.v[turn][i][lane] : 0.0f);
+    for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+    if ((lane & 15) == 0) s.v[turn][half][warp] = t;
+    __syncthreads();
+    t = (lane & 15) < nwarps ? s.v[turn][half][lane & 15] : 0.0f;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+    v[0] = __shfl_sync(0xFFFFFFFFu, t, 0);
+    v[1] = __shfl_sync(0xFFFFFFFFu, t, 16);
 }
 
 // One kernel launch with the library's programmatic dependent launch option.
@@ -150,6 +185,18 @@ template <class T> struct Slot {
             return __uint_as_float((i & 1) ? (u & 0xFFFF0000u) : (u << 16));
         }
     }
+    // elements 2 p and 2 p + 1 as an f32 pair, for the two-lane arithmetic
+    __device__ __forceinline__ uint64_t pair(int p) const { return f2_pack(get(2 * p), get(2 * p + 1)); }
+    __device__ __forceinline__ void put_pair(int p, uint64_t v) {
+        float lo, hi;
+        f2_unpack(v, lo, hi);
+        if constexpr (T::kBytes == 4) {
+            w[2 * p] = __float_as_uint(lo);
+            w[2 * p + 1] = __float_as_uint(hi);
+        } else {
+            w[p] = pack_bf16x2(lo, hi);
+        }
+    }
     // rounds to T (to nearest even)
     __device__ __forceinline__ void put(const float (&f)[8]) {
         if constexpr (T::kBytes == 4) {
@@ -177,6 +224,17 @@ template <class T> struct Slot {
         }
     }
 };
+
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float f2_sum(uint64_t v) {
+    float lo, hi;
+    f2_unpack(v, lo, hi);
+    return lo + hi;
+}
 
 // A whole slot, aligned to its size; read once (past L1).
 __device__ __forceinline__ void ld_slot(Slot<BF16> &s, const void *p) {
