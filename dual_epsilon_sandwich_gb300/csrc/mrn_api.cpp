@@ -22,6 +22,7 @@
 
 #include "mrn_checks.h"
 #include "mrn_internal.h"
+#include "mrn_train.h"
 
 namespace {
 
@@ -63,6 +64,10 @@ int sm_count_of_current_device() {
 }
 
 bool launch_pdl() { return (t_launch_options & MRN_LAUNCH_PDL) != 0; }
+
+uint32_t launch_stall_bytes() {
+    return (t_launch_options & MRN_LAUNCH_TEST_WAIT_TIMEOUT) ? 16u : 0u;
+}
 
 mrn_status launch_result(cudaError_t err, uint64_t launched) {
     g_launch_count.fetch_add(launched, std::memory_order_relaxed);
@@ -597,7 +602,7 @@ mrn_status launch(const Call &c, bool aligned16, cudaStream_t stream) {
     }
     g.pdl = (t_launch_options & MRN_LAUNCH_PDL) ? 1 : 0;
     KernelArgs a = c.args;
-    a.stall_bytes = (t_launch_options & MRN_LAUNCH_TEST_WAIT_TIMEOUT) ? 16u : 0u;
+    a.stall_bytes = launch_stall_bytes();
     a.n = c.n;
     a.nvec = ceil_div(c.n, g.vec);
     const bool bf16 = c.dt == MRN_BF16;
@@ -963,7 +968,9 @@ int mrn_wait_timeouts(void) {
                           mrn::take_wait_timeouts_then_add_scale(),
                           mrn::take_wait_timeouts_rmsnorm_q8_1(),
                           mrn::take_wait_timeouts_seam_f16(),
-                          mrn::take_wait_timeouts_seam_bf16()};
+                          mrn::take_wait_timeouts_seam_bf16(),
+                          mrn::take_wait_timeouts_layernorm(),
+                          mrn::take_wait_timeouts_norm_backward()};
     int total = 0;
     for (int v : counts) {
         if (v < 0) {

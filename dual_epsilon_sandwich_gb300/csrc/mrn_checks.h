@@ -45,6 +45,8 @@ inline bool aligned_to(const void *p, int64_t a) { return reinterpret_cast<uintp
 int sm_count_of_current_device();
 // The calling thread's launch option MRN_LAUNCH_PDL.
 bool launch_pdl();
+// ... and 16 with MRN_LAUNCH_TEST_WAIT_TIMEOUT, else 0.
+uint32_t launch_stall_bytes();
 // Counts a call's launches and turns its CUDA error into a status.
 mrn_status launch_result(cudaError_t err, uint64_t launched);
 

@@ -10,6 +10,16 @@
 namespace mrn {
 
 constexpr int kLoopedThreads = 512;
+// Threads that an SM's registers are shared between (the launch bound), from what a thread
+// holds: k slots of r rows and of two weights.
+template <class T> constexpr int forward_resident(int k, int r) {
+    const int words = k * (r + 2) * Slot<T>::kWords;
+    return words <= 12 ? 1024 : (words <= 28 ? 768 : (words <= 36 ? 640 : (words <= 68 ? 512 : (words <= 100 ? 384 : 256))));
+}
+// Threads of a CTA at most.
+template <class T> constexpr int forward_threads(int k, int r) {
+    return forward_resident<T>(k, r) < 512 ? forward_resident<T>(k, r) : 512;
+}
 
 // Any width: one row per CTA at a time, three passes over it (the second and
 // third out of L2), element by element.
@@ -55,27 +65,28 @@ __global__ void __launch_bounds__(kLoopedThreads) mrn_layernorm_looped_kernel(co
     }
 }
 
-// The row held in registers between its copy and its outputs (see mrn_row_tile.cuh).
-template <class T, int K, bool EDGE, bool WARP, bool ADD>
-__global__ void __launch_bounds__(WARP ? 128 : tile_max_threads(K))
+// Rows held in registers between their copy and their outputs (see mrn_row_tile.cuh).
+template <class T, int K, int R, bool EDGE, bool WARP, bool ADD>
+__global__ void __launch_bounds__(forward_resident<T>(K, R))
 mrn_layernorm_tile_kernel(const LayernormArgs a, const TileArgs t) {
     extern __shared__ __align__(16) unsigned char ring_bytes[];
-    __shared__ RowSumSlots<1> slots;
-    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(ring_bytes));
-    RowTile<T, K, EDGE, WARP> tile(a.rows, a.n, t);
+    __shared__ RowSumSlots<R> slots;
     constexpr int kOps = ADD ? 2 : 1;
+    __shared__ EndSlots<kOps, R, EDGE, WARP> end_w;
+    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(ring_bytes));
+    RowTile<T, K, R, EDGE, WARP> tile(a.rows, a.n, t);
     const int64_t back = static_cast<int64_t>(t.mis) * T::kBytes;
-    const char *const ops[kTileMaxOperands] = {static_cast<const char *>(a.x) - back,
-                                               ADD ? static_cast<const char *>(a.res) - back : nullptr,
-                                               nullptr};
+    const char *ops[kOps];
+    ops[0] = static_cast<const char *>(a.x) - back;
+    if constexpr (ADD) ops[1] = static_cast<const char *>(a.res) - back;
     char *const y = static_cast<char *>(a.y) - back;
     char *const stream_out = ADD ? static_cast<char *>(a.stream_out) - back : nullptr;
-    RingWalk walk(kOps * K * tile.region, t.stages);
+    RingWalk walk(R * kOps * K * tile.region, t.stages);
     const int ahead = t.stages - 1;
     tile.clear(ring, t.stages, kOps);
-    if (tile.cl > 1) cluster_arrive_relaxed();   // (peers' shared memory is written later)
+    row_sum_setup(slots, tile.cl);
     pdl_enter();
-    for (int s = 0; s < ahead; ++s) tile.issue(ring + s * walk.bytes, s, ops, kOps);
+    for (int s = 0; s < ahead; ++s) tile.issue(ring + s * walk.bytes, s, s, ops, kOps, end_w);
     const DropKey key = ADD ? drop_key(a.drop) : DropKey{};
     Slot<T> gamma[K], beta[K];
     tile.weights(gamma, a.gamma);
@@ -85,103 +96,153 @@ mrn_layernorm_tile_kernel(const LayernormArgs a, const TileArgs t) {
 #pragma unroll
         for (int k = 0; k < K; ++k) beta[k].zero();
     }
-    if (tile.cl > 1) cluster_wait_acquire();
+    const float end_gamma = EDGE ? tile.end_weight(a.gamma) : 0.0f;
+    const float end_beta = EDGE && a.beta ? tile.end_weight(a.beta) : 0.0f;
+    row_sum_ready(tile.cl);
     const float inv_n = 1.0f / static_cast<float>(a.n);
     int turn = 0;
-    for (; tile.cta_row() < a.rows; tile.advance(), walk.next()) {
+    for (; tile.cta_left > 0; tile.advance(), walk.next()) {
         __syncwarp();
-        tile.issue(ring + walk.write * walk.bytes, ahead, ops, kOps);
+        tile.issue(ring + walk.write * walk.bytes, walk.write, ahead, ops, kOps, end_w);
         cp_async_wait(ahead);
         __syncwarp();
         const uint32_t from = ring + walk.read * walk.bytes;
-        Slot<T> v[K];
-        tile.fetch(v, from, 0);
-        if constexpr (ADD) {
-            Slot<T> res[K];
-            tile.fetch(res, from, 1);
+        Slot<T> v[R][K];
+        float sum[R], end[R];
+#pragma unroll
+        for (int rr = 0; rr < R; ++rr) {
+            tile.fetch(v[rr], from, 0, rr, kOps);
+            if constexpr (ADD) {
+                Slot<T> res[K];
+                tile.fetch(res, from, 1, rr, kOps);
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const DropGroup d = drop_group(key, tile.group(rr, k), a.drop.threshold);
+                    float o[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        o[i] = drop_add(v[rr][k].get(i), res[k].get(i), d.keeps(i), a.drop.scale);
+                    v[rr][k].put(o);
+                }
+                tile.store(stream_out, rr, tile.valid(rr), v[rr]);
+            }
+            uint64_t acc = 0;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                if (tile.in[k] == 0u) continue;
-                const DropGroup d = drop_group(key, tile.group(k), a.drop.threshold);
-                float o[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    o[i] = drop_add(v[k].get(i), res[k].get(i), d.keeps(i), a.drop.scale);
-                v[k].put(o);
-                if (!WARP || tile.row < a.rows) tile.store(stream_out, k, v[k]);
+                for (int i = 0; i < 4; ++i) acc = f2_add(acc, v[rr][k].pair(i));
+            }
+            sum[rr] = f2_sum(acc);
+            end[rr] = 0.0f;
+            if (EDGE && tile.ends) {
+                end[rr] = tile.fetch_end(end_w, walk.read, 0, rr);
+                if constexpr (ADD) {
+                    const bool keep = drop_keeps_element(key, tile.end_element(rr), a.drop.threshold);
+                    end[rr] = tile.store_end(stream_out, rr, tile.valid(rr),
+                                             drop_add(end[rr], tile.fetch_end(end_w, walk.read, 1, rr),
+                                                      keep, a.drop.scale));
+                    if (tile.end_col < 0) end[rr] = 0.0f;
+                }
+                sum[rr] += end[rr];
             }
         }
-        uint64_t acc = 0;
+        if (!row_sum<R, WARP>(sum, slots, turn, tile.width, tile.cl, tile.crank, turn == 0 ? t.stall : 0u)) break;
+        float dev[R];
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
+        for (int rr = 0; rr < R; ++rr) {
+            sum[rr] *= inv_n;     // the mean
+            const uint64_t minus = f2_pack(-sum[rr], -sum[rr]);
+            uint64_t acc = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc = f2_add(acc, v[k].pair(i));
-        }
-        float sum[1] = {f2_sum(acc)};
-        row_sum<1, WARP>(sum, slots, turn, tile.width, tile.cl, tile.crank);
-        const float mean = sum[0] * inv_n;
-        const uint64_t minus = f2_pack(-mean, -mean);
-        acc = 0;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            if (tile.in[k] == 0u) continue;
-            if (!EDGE || tile.in[k] == 0xFFu) {
+            for (int k = 0; k < K; ++k) {
+                uint64_t part = 0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint64_t d = f2_add(v[k].pair(i), minus);
-                    acc = f2_fma(d, d, acc);
+                    const uint64_t d = f2_add(v[rr][k].pair(i), minus);
+                    part = f2_fma(d, d, part);
                 }
-            } else {
-                float part = 0.0f;
+                acc = f2_add(acc, tile.holds(k) ? part : 0);
+            }
+            dev[rr] = f2_sum(acc);
+            if (EDGE && tile.end_col >= 0) dev[rr] = fmaf(end[rr] - sum[rr], end[rr] - sum[rr], dev[rr]);
+        }
+        if (!row_sum<R, WARP>(dev, slots, turn, tile.width, tile.cl, tile.crank, 0u)) break;
+        uint64_t minus[R], scale[R];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float d = ((tile.in[k] >> i) & 1u) ? v[k].get(i) - mean : 0.0f;
-                    part = fmaf(d, d, part);
-                }
-                acc = f2_add(acc, f2_pack(part, 0.0f));
+        for (int rr = 0; rr < R; ++rr) {
+            const float rstd = inv_sqrt(fmaf(dev[rr], inv_n, a.eps));
+            if (a.mean && tile.first == 0 && tile.valid(rr)) {
+                a.mean[tile.row + rr * tile.stride] = sum[rr];
+                a.rstd[tile.row + rr * tile.stride] = rstd;
+            }
+            minus[rr] = f2_pack(-sum[rr], -sum[rr]);
+            scale[rr] = f2_pack(rstd, rstd);
+            if (EDGE && tile.ends)
+                tile.store_end(y, rr, tile.valid(rr), fmaf((end[rr] - sum[rr]) * rstd, end_gamma, end_beta));
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint64_t g = gamma[k].pair(i), b = beta[k].pair(i);
+#pragma unroll
+                for (int rr = 0; rr < R; ++rr)
+                    v[rr][k].put_pair(i, f2_fma(f2_mul(f2_add(v[rr][k].pair(i), minus[rr]), scale[rr]), g, b));
             }
         }
-        float dev[1] = {f2_sum(acc)};
-        row_sum<1, WARP>(dev, slots, turn, tile.width, tile.cl, tile.crank);
-        const float rstd = inv_sqrt(fmaf(dev[0], inv_n, a.eps));
-        if (!WARP || tile.row < a.rows) {
-            if (a.mean && tile.first == 0) {
-                a.mean[tile.row] = mean;
-                a.rstd[tile.row] = rstd;
-            }
-            const uint64_t scale = f2_pack(rstd, rstd);
 #pragma unroll
-            for (int k = 0; k < K; ++k) {
-                Slot<T> out;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    out.put_pair(i, f2_fma(f2_mul(f2_add(v[k].pair(i), minus), scale),
-                                           gamma[k].pair(i), beta[k].pair(i)));
-                tile.store(y, k, out);
-            }
-        }
+        for (int rr = 0; rr < R; ++rr) tile.store(y, rr, tile.valid(rr), v[rr]);
     }
     cp_async_wait(0);
+    row_sum_leave(tile.cl);
 }
 
-template <class T, int K, bool EDGE, bool WARP, bool ADD>
-cudaError_t launch_layernorm_tile(const LayernormArgs &a, const TilePlan &p, bool pdl,
-                                  cudaStream_t stream, uint64_t *launches) {
+// Whether the call was launched; false: it takes the looped kernel.
+template <class T, int K, int R, bool EDGE, bool WARP, bool ADD>
+bool launch_layernorm_tile(const LayernormArgs &a, const TileShape &p, int sms, bool pdl,
+                           cudaStream_t stream, uint64_t *launches, cudaError_t *err) {
     static TileLaunchCache cache;
-    const TileArgs t = {p.lanes, p.stages, p.mis};
-    const int64_t shared = tile_ring_bytes(T::kBytes, K, p.threads, p.stages, ADD ? 2 : 1);
-    return launch_tile(cache, mrn_layernorm_tile_kernel<T, K, EDGE, WARP, ADD>, p, shared, pdl,
+    const auto fn = mrn_layernorm_tile_kernel<T, K, R, EDGE, WARP, ADD>;
+    constexpr int kOps = ADD ? 2 : 1;
+    int resident = 0;
+    *err = open_tile(cache, fn, p.threads, &resident);
+    if (*err != cudaSuccess) return true;
+    const TileGrid g = tile_grid(p, a.rows, R, T::kBytes, kOps, resident, 32, sms);
+    if (g.stages < 1) return false;
+    const TileArgs t = {p.lanes, g.stages, p.mis, a.stall};
+    *err = launch_tile(fn, p, g.ctas, tile_ring_bytes(T::kBytes, K, p.threads, g.stages, kOps * R), pdl,
                        stream, launches, a, t);
+    return true;
 }
 
-template <class T, int K, bool WARP>
-cudaError_t launch_layernorm_k(const LayernormArgs &a, const TilePlan &p, bool pdl,
-                               cudaStream_t stream, uint64_t *launches) {
+template <class T, int K, int R, bool WARP>
+bool launch_layernorm_k(const LayernormArgs &a, const TileShape &p, int sms, bool pdl,
+                        cudaStream_t stream, uint64_t *launches, cudaError_t *err) {
     if (a.res)
-        return p.edge ? launch_layernorm_tile<T, K, true, WARP, true>(a, p, pdl, stream, launches)
-                      : launch_layernorm_tile<T, K, false, WARP, true>(a, p, pdl, stream, launches);
-    return p.edge ? launch_layernorm_tile<T, K, true, WARP, false>(a, p, pdl, stream, launches)
-                  : launch_layernorm_tile<T, K, false, WARP, false>(a, p, pdl, stream, launches);
+        return p.edge ? launch_layernorm_tile<T, K, R, true, WARP, true>(a, p, sms, pdl, stream, launches, err)
+                      : launch_layernorm_tile<T, K, R, false, WARP, true>(a, p, sms, pdl, stream, launches, err);
+    return p.edge ? launch_layernorm_tile<T, K, R, true, WARP, false>(a, p, sms, pdl, stream, launches, err)
+                  : launch_layernorm_tile<T, K, R, false, WARP, false>(a, p, sms, pdl, stream, launches, err);
+}
+
+// Slots per thread and rows at a time for rows of a CTA.  Measured on GB300, a 200 to 250 MB
+// call each, against the next best of k = 1..4, r = 1..2 (us):
+//   bf16, alone:      n = 2048 2 x 2 32.7 (4 x 1 33.3), 4096 4 x 1 33.4 (2 x 2 35.5), 8192 4 x 1
+//                     32.3 (2 x 2 37.4), 16384 4 x 1 54.6 (4 x 2 57.5)
+//   bf16, after add:  n = 4096 2 x 2 64.6 (2 x 1 65.5), 5120 4 x 1 65.8 (2 x 2 66.2), 8192 4 x 1
+//                     63.8 (2 x 2 65.3)
+//   f32, alone:       n = 4096 1 x 1 32.2 (3 x 1 32.8), 8192 2 x 2 32.8 (4 x 2 32.9), 12288 4 x 1
+//                     50.3 (3 x 1 58.4)
+//   f32, after add:   n = 4096 1 x 1 63.0 (3 x 2 64.9), 6656 4 x 1 63.8 (3 x 1 65.3)
+template <class T> void forward_tile(int64_t slots, bool add, int *k, int *r) {
+    if (T::kBytes == 2) {
+        const bool narrow = slots <= (add ? 576 : 320);
+        *k = narrow ? 2 : 4;
+        *r = narrow ? 2 : 1;
+    } else {
+        *k = slots <= 512 ? 1 : (slots <= 1024 && !add ? 2 : 4);
+        *r = *k == 2 ? 2 : 1;
+    }
 }
 
 template <class T>
@@ -190,19 +251,26 @@ cudaError_t launch_layernorm_typed(const LayernormArgs &a, int sms, bool pdl, cu
     const int mis = common_offset(T::kBytes, a.x, a.y, a.res, static_cast<const void *>(a.stream_out));
     // (a generator group is a slot only when the operands start on a slot boundary)
     if (mis == 0 || (mis > 0 && a.drop.threshold == 0)) {
-        const TileWish wish = {a.res ? 2 : 1, 2, 1024, 8};
-        const TilePlan p = plan_tiles(a.rows, a.n, T::kBytes, mis, wish, sms);
+        int k = 4, r = 1;
+        forward_tile<T>(a.n / 8, a.res != nullptr, &k, &r);
+        //KR
+        const bool few = tile_few_rows(a.rows, a.n, sms);
+        if (few) k = r = 1;
+        const TileShape p = tile_shape(a.n, mis, k, few ? tile_few_threads(a.rows, a.n, sms) : forward_threads<T>(k, r), few);
+        cudaError_t err = cudaSuccess;
+        bool done = false;
         if (p.ok && p.warp) {
-            if (p.k == 1) return launch_layernorm_k<T, 1, true>(a, p, pdl, stream, launches);
-            if (p.k == 2) return launch_layernorm_k<T, 2, true>(a, p, pdl, stream, launches);
-            return launch_layernorm_k<T, 4, true>(a, p, pdl, stream, launches);
+            done = p.k == 1   ? launch_layernorm_k<T, 1, 1, true>(a, p, sms, pdl, stream, launches, &err)
+                   : p.k == 2 ? launch_layernorm_k<T, 2, 1, true>(a, p, sms, pdl, stream, launches, &err)
+                   : p.k == 3 ? launch_layernorm_k<T, 3, 1, true>(a, p, sms, pdl, stream, launches, &err)
+                              : launch_layernorm_k<T, 4, 1, true>(a, p, sms, pdl, stream, launches, &err);
+        } else if (p.ok) {
+            //MORE
+            if (k == 1) done = launch_layernorm_k<T, 1, 1, false>(a, p, sms, pdl, stream, launches, &err);
+            else if (k == 2) done = launch_layernorm_k<T, 2, 2, false>(a, p, sms, pdl, stream, launches, &err);
+            else done = launch_layernorm_k<T, 4, 1, false>(a, p, sms, pdl, stream, launches, &err);
         }
-        if (p.ok) {
-            if (p.k == 1) return launch_layernorm_k<T, 1, false>(a, p, pdl, stream, launches);
-            if (p.k == 2) return launch_layernorm_k<T, 2, false>(a, p, pdl, stream, launches);
-            if (p.k == 3) return launch_layernorm_k<T, 3, false>(a, p, pdl, stream, launches);
-            return launch_layernorm_k<T, 4, false>(a, p, pdl, stream, launches);
-        }
+        if (done) return err;
     }
     const int64_t ctas = a.rows < 4LL * sms ? a.rows : 4LL * sms;
     return launch_plain(mrn_layernorm_looped_kernel<T>, ctas, kLoopedThreads, 0, pdl, stream,
@@ -214,5 +282,7 @@ cudaError_t launch_layernorm(bool bf16, const LayernormArgs &a, int sms, bool pd
     return bf16 ? launch_layernorm_typed<BF16>(a, sms, pdl, stream, launches)
                 : launch_layernorm_typed<F32>(a, sms, pdl, stream, launches);
 }
+
+int take_wait_timeouts_layernorm() { return take_wait_timeouts<kOpLayernormTimeouts>(); }
 
 }  // namespace mrn

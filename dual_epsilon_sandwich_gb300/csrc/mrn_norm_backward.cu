@@ -16,6 +16,10 @@ namespace mrn {
 
 constexpr int kLoopedThreads = 512;
 
+// Threads that an SM's registers are shared between (the launch bound): what a thread with k
+// slots needs.
+constexpr int backward_resident(int k) { return k <= 1 ? 768 : (k <= 2 ? 512 : (k <= 3 ? 384 : 256)); }
+
 // A backward pass leaves at most this many partial rows, and for very wide rows
 // no more than fill 2^27 floats.
 constexpr int kPartsPerSm = 4;
@@ -90,20 +94,21 @@ mrn_norm_backward_looped_kernel(const BackwardArgs a, float *part_gamma, float *
     }
 }
 
-// The row held in registers between its copy and its outputs, the column sums in
+// Rows held in registers between their copy and their outputs, the column sums in
 // registers over all rows of the CTA (see mrn_row_tile.cuh).
 template <class T, int K, bool EDGE, bool WARP, bool RMS>
-__global__ void __launch_bounds__(WARP ? 128 : tile_max_threads(K))
+__global__ void __launch_bounds__(backward_resident(K))
 mrn_norm_backward_tile_kernel(const BackwardArgs a, const TileArgs t, float *part_gamma,
                               float *part_beta, const int64_t part_stride) {
     extern __shared__ __align__(16) unsigned char ring_bytes[];
     __shared__ RowSumSlots<2> slots;
-    __shared__ float stats[kTileMaxStages][2][128];   // mean and rstd of the ring's rows, per team
+    __shared__ float stats[kTileMaxStages][2][kWarpTileThreads];   // mean and rstd, per team
+    __shared__ EndSlots<3, 1, EDGE, WARP> end_w;
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(ring_bytes));
-    RowTile<T, K, EDGE, WARP> tile(a.rows, a.n, t);
+    RowTile<T, K, 1, EDGE, WARP> tile(a.rows, a.n, t);
     const int ops_count = a.dstream ? 3 : 2;
     const int64_t back = static_cast<int64_t>(t.mis) * T::kBytes;
-    const char *const ops[kTileMaxOperands] = {
+    const char *const ops[3] = {
         static_cast<const char *>(a.dy) - back, static_cast<const char *>(a.x) - back,
         a.dstream ? static_cast<const char *>(a.dstream) - back : nullptr};
     char *const dx = static_cast<char *>(a.dx) - back;
@@ -111,16 +116,17 @@ mrn_norm_backward_tile_kernel(const BackwardArgs a, const TileArgs t, float *par
     RingWalk walk(ops_count * K * tile.region, t.stages);
     const int ahead = t.stages - 1;
     tile.clear(ring, t.stages, ops_count);
-    if (tile.cl > 1) cluster_arrive_relaxed();   // (peers' shared memory is written later)
+    row_sum_setup(slots, tile.cl);
     pdl_enter();
-    // mean and rstd travel with their row, so that no load of them is waited for
-    auto issue = [&](int to, int rows_ahead) {
-        const int64_t r = tile.row + rows_ahead * tile.stride;
-        if (!RMS && tile.leads && r < a.rows) {
+    // mean and rstd travel with their row: a load of them in the loop held up every row
+    // (16384 x 4096 bf16: 116 us against 80)
+    auto issue = [&](int to, int turns) {
+        if (!RMS && tile.leads && turns < tile.left) {
+            const int64_t r = tile.row + turns * tile.stride;
             cp_async4(static_cast<uint32_t>(__cvta_generic_to_shared(&stats[to][0][tile.team])), a.mean + r);
             cp_async4(static_cast<uint32_t>(__cvta_generic_to_shared(&stats[to][1][tile.team])), a.rstd + r);
         }
-        tile.issue(ring + to * walk.bytes, rows_ahead, ops, ops_count);
+        tile.issue(ring + to * walk.bytes, to, turns, ops, ops_count, end_w);
     };
     for (int s = 0; s < ahead; ++s) issue(s, s);
     const DropKey key = drop_key(a.drop);
@@ -131,24 +137,26 @@ mrn_norm_backward_tile_kernel(const BackwardArgs a, const TileArgs t, float *par
     for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum_g[k][i] = sum_b[k][i] = 0;
+    const float end_gamma = EDGE ? tile.end_weight(a.gamma) : 0.0f;
+    float end_sum_g = 0.0f, end_sum_b = 0.0f;
     const float inv_n = 1.0f / static_cast<float>(a.n);
     int turn = 0;
-    if (tile.cl > 1) cluster_wait_acquire();
-    for (; tile.cta_row() < a.rows; tile.advance(), walk.next()) {
+    row_sum_ready(tile.cl);
+    for (; tile.cta_left > 0; tile.advance(), walk.next()) {
         __syncwarp();
         issue(walk.write, ahead);
         cp_async_wait(ahead);
         __syncwarp();
         const uint32_t from = ring + walk.read * walk.bytes;
-        Slot<T> dy[K], x[K];
-        tile.fetch(dy, from, 0);
-        tile.fetch(x, from, 1);
-        const bool ok = !WARP || tile.row < a.rows;
-        const float mean = RMS || !ok ? 0.0f : stats[walk.read][0][tile.team];
-        float rstd = RMS || !ok ? 0.0f : stats[walk.read][1][tile.team];
+        const bool ok = !WARP || tile.valid(0);
         // w = dy gamma and xh (RMSNorm: x) stay until the outputs.
         // LayerNorm: sums of w and w xh; RMSNorm: of x^2 and w x
         uint64_t w[K][4], xh[K][4];
+        Slot<T> dy[K], x[K];
+        tile.fetch(dy, from, 0, 0, ops_count);
+        tile.fetch(x, from, 1, 0, ops_count);
+        const float mean = RMS || !ok ? 0.0f : stats[walk.read][0][tile.team];
+        float rstd = RMS || !ok ? 0.0f : stats[walk.read][1][tile.team];
         uint64_t s0 = 0, s1 = 0;
         const uint64_t minus = f2_pack(-mean, -mean);
         uint64_t scale = f2_pack(rstd, rstd);
@@ -171,63 +179,100 @@ mrn_norm_backward_tile_kernel(const BackwardArgs a, const TileArgs t, float *par
             }
         }
         float s[2] = {f2_sum(s0), f2_sum(s1)};
-        row_sum<2, WARP>(s, slots, turn, tile.width, tile.cl, tile.crank);
+        float end_d = 0.0f, end_xh = 0.0f;
+        if (EDGE && tile.ends) {
+            end_d = tile.fetch_end(end_w, walk.read, 0, 0);
+            end_xh = tile.fetch_end(end_w, walk.read, 1, 0);
+            const float ew = end_d * end_gamma;
+            if (RMS) {
+                s[0] = fmaf(end_xh, end_xh, s[0]);
+            } else {
+                // (lanes without an element have d = 0, and xh is then of no effect)
+                end_xh = (end_xh - mean) * rstd;
+                s[0] += ew;
+                end_sum_g = fmaf(end_d, end_xh, end_sum_g);
+                end_sum_b += end_d;
+            }
+            s[1] = fmaf(ew, end_xh, s[1]);
+        }
+        if (!row_sum<2, WARP>(s, slots, turn, tile.width, tile.cl, tile.crank, turn == 0 ? t.stall : 0u)) break;
         // ds = rstd w - rstd c1 - xh rstd c2
         float c1 = 0.0f, c2;
         if (RMS) {
             rstd = inv_sqrt(fmaf(s[0], inv_n, a.eps));
             scale = f2_pack(rstd, rstd);
             c2 = -(s[1] * inv_n * rstd) * rstd * rstd;
+            // dy once more, for dgamma
+            tile.fetch(dy, from, 0, 0, ops_count);
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sum_g[k][i] = f2_fma(dy[k].pair(i), f2_mul(xh[k][i], scale), sum_g[k][i]);
         } else {
             c1 = -(s[0] * inv_n) * rstd;
             c2 = -(s[1] * inv_n) * rstd;
         }
         const uint64_t c1p = f2_pack(c1, c1), c2p = f2_pack(c2, c2);
-        if (a.dstream) tile.fetch(x, from, 2);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            uint64_t o[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                o[i] = f2_fma(xh[k][i], c2p, RMS ? f2_mul(w[k][i], scale)
-                                                 : f2_fma(w[k][i], scale, c1p));
-                if (RMS) sum_g[k][i] = f2_fma(dy[k].pair(i), f2_mul(xh[k][i], scale), sum_g[k][i]);
-            }
-            if (a.dstream) {
+            for (int i = 0; i < 4; ++i)
+                w[k][i] = f2_fma(xh[k][i], c2p, RMS ? f2_mul(w[k][i], scale) : f2_fma(w[k][i], scale, c1p));
+        }
+        if (a.dstream) {
+            tile.fetch(x, from, 2, 0, ops_count);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) o[i] = f2_add(o[i], x[k].pair(i));
-            }
-            if (!ok) continue;
-            Slot<T> out;
+            for (int k = 0; k < K; ++k)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) out.put_pair(i, o[i]);
+                for (int i = 0; i < 4; ++i) w[k][i] = f2_add(w[k][i], x[k].pair(i));
+        }
+        Slot<T> out[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) out[k].put_pair(i, w[k][i]);
+        if (EDGE && tile.ends) {
+            const float ew = end_d * end_gamma;
+            float o = fmaf(end_xh, c2, RMS ? ew * rstd : fmaf(ew, rstd, c1));
+            if (RMS) end_sum_g = fmaf(end_d, end_xh * rstd, end_sum_g);
+            if (a.dstream) o += tile.fetch_end(end_w, walk.read, 2, 0);
             if (a.dres) {
-                tile.store(dres, k, out);
-                if (tile.in[k] != 0u) {
-                    const DropGroup g = drop_group(key, tile.group(k), a.drop.threshold);
+                tile.store_end(dres, 0, ok, o);
+                const bool keep = drop_keeps_element(key, tile.end_element(0), a.drop.threshold);
+                o = drop_scale(o, keep, a.drop.scale);
+            }
+            tile.store_end(dx, 0, ok, o);
+        }
+        if (a.dres) {
+            tile.store(dres, 0, ok, out);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float lo, hi;
-                        f2_unpack(o[i], lo, hi);
-                        out.put_pair(i, f2_pack(drop_scale(lo, g.keeps(2 * i), a.drop.scale),
-                                                drop_scale(hi, g.keeps(2 * i + 1), a.drop.scale)));
-                    }
+            for (int k = 0; k < K; ++k) {
+                const DropGroup g = drop_group(key, tile.group(0, k), a.drop.threshold);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float lo, hi;
+                    f2_unpack(w[k][i], lo, hi);
+                    out[k].put_pair(i, f2_pack(drop_scale(lo, g.keeps(2 * i), a.drop.scale),
+                                               drop_scale(hi, g.keeps(2 * i + 1), a.drop.scale)));
                 }
             }
-            tile.store(dx, k, out);
         }
+        tile.store(dx, 0, ok, out);
     }
     cp_async_wait(0);
+    row_sum_leave(tile.cl);
+    // Column j of a partial row stands at j + 8 - before, so that slots are aligned; the join
+    // knows `before` from the row's number.
     if constexpr (!WARP) {
-        // one partial row per CTA (or cluster), in slots: the join knows the row's offset
         const int64_t part = blockIdx.x / tile.cl;
 #pragma unroll
         for (int which = 0; which < (RMS ? 1 : 2); ++which) {
             if (which == 1 && !part_beta) break;
-            float *const out = (which == 0 ? part_gamma : part_beta) + part * part_stride;
+            float *const out = (which == 0 ? part_gamma : part_beta) + part * part_stride + (EDGE ? 8 : 0);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                if (tile.in[k] == 0u) continue;
+                if (!tile.holds(k)) continue;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     Frag<F32, 4> v;
@@ -238,11 +283,13 @@ mrn_norm_backward_tile_kernel(const BackwardArgs a, const TileArgs t, float *par
                     st_global(out + (tile.first + k * tile.width) * 8 + 4 * i, v);
                 }
             }
+            if (EDGE && tile.end_col >= 0)
+                out[tile.end_col - tile.before] = which == 0 ? end_sum_g : end_sum_b;
         }
     } else {
-        // the rows' sums of this CTA through the ring, in slots; then one column per thread,
-        // over the rows in order
-        const int span = K * tile.width * 8;
+        // the rows' sums of this CTA through the ring, laid out the same; then one column per
+        // thread, over the rows in order
+        const int span = K * tile.width * 8 + (EDGE ? 16 : 0);
         const int teams = static_cast<int>(blockDim.x) / tile.width;
         const int64_t row0 = static_cast<int64_t>(blockIdx.x) * teams;
         float *const buf = reinterpret_cast<float *>(ring_bytes);
@@ -250,20 +297,23 @@ mrn_norm_backward_tile_kernel(const BackwardArgs a, const TileArgs t, float *par
         for (int which = 0; which < (RMS ? 1 : 2); ++which) {
             if (which == 1 && !part_beta) break;
             __syncthreads();
+            float *const mine = buf + tile.team * span + (EDGE ? 8 : 0);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                uint64_t *to = reinterpret_cast<uint64_t *>(buf + tile.team * span +
-                                                            (tile.first + k * tile.width) * 8);
+                if (!tile.holds(k)) continue;
+                uint64_t *to = reinterpret_cast<uint64_t *>(mine + (tile.first + k * tile.width) * 8);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) to[i] = which == 0 ? sum_g[k][i] : sum_b[k][i];
             }
+            if (EDGE && tile.end_col >= 0)
+                mine[tile.end_col - tile.before] = which == 0 ? end_sum_g : end_sum_b;
             __syncthreads();
             float *const out = (which == 0 ? part_gamma : part_beta) +
                                static_cast<int64_t>(blockIdx.x) * part_stride;
             for (int j = threadIdx.x; j < static_cast<int>(a.n); j += blockDim.x) {
                 float v = 0.0f;
                 for (int g = 0; g < teams; ++g) {
-                    const int off = EDGE ? static_cast<int>((t.mis + (row0 + g) * a.n) & 7) : 0;
+                    const int off = EDGE ? 8 - static_cast<int>(-(t.mis + (row0 + g) * a.n) & 7) : 0;
                     v += buf[g * span + j + off];
                 }
                 out[j] = v;
@@ -272,34 +322,52 @@ mrn_norm_backward_tile_kernel(const BackwardArgs a, const TileArgs t, float *par
     }
 }
 
+struct BackwardLaunch {
+    int sms;
+    bool pdl;
+    cudaStream_t stream;
+    uint64_t *launches;
+    int64_t most_parts;
+    int64_t parts;      // out: partial rows written
+    cudaError_t err;    // out
+};
+
+// Whether the call was launched; false: it takes the looped kernel.
 template <class T, int K, bool EDGE, bool WARP, bool RMS>
-cudaError_t launch_backward_tile(const BackwardArgs &a, const TilePlan &p, float *pg, float *pb,
-                                 bool pdl, cudaStream_t stream, uint64_t *launches) {
+bool launch_backward_tile(const BackwardArgs &a, const TileShape &p, BackwardLaunch &l) {
     static TileLaunchCache cache;
-    const TileArgs t = {p.lanes, p.stages, p.mis};
-    const int64_t shared = tile_ring_bytes(T::kBytes, K, p.threads, p.stages, a.dstream ? 3 : 2);
-    return launch_tile(cache, mrn_norm_backward_tile_kernel<T, K, EDGE, WARP, RMS>, p, shared, pdl,
-                       stream, launches, a, t, pg, pb, part_stride_of(a.n));
+    const auto fn = mrn_norm_backward_tile_kernel<T, K, EDGE, WARP, RMS>;
+    const int operands = a.dstream ? 3 : 2;
+    int resident = 0;
+    l.err = open_tile(cache, fn, p.threads, &resident);
+    if (l.err != cudaSuccess) return true;
+    const TileGrid g = tile_grid(p, a.rows, 1, T::kBytes, operands, resident, kPartsPerSm, l.sms);
+    l.parts = g.ctas / p.cluster;
+    if (g.stages < 1 || l.parts > l.most_parts) return false;   // (the workspace holds no more)
+    const TileArgs t = {p.lanes, g.stages, p.mis, a.stall};
+    const int64_t stride = part_stride_of(a.n);
+    // (WARP: the epilogue's rows have room for the ends)
+    const int64_t shared = tile_ring_bytes(T::kBytes, K, p.threads, g.stages, operands) + (WARP ? 1024 : 0);
+    l.err = launch_tile(fn, p, g.ctas, shared,
+                        l.pdl, l.stream, l.launches, a, t, a.workspace,
+                        a.dbeta ? a.workspace + l.parts * stride : nullptr, stride);
+    return true;
 }
 
 template <class T, int K, bool WARP>
-cudaError_t launch_backward_k(const BackwardArgs &a, const TilePlan &p, float *pg, float *pb,
-                              bool pdl, cudaStream_t stream, uint64_t *launches) {
+bool launch_backward_k(const BackwardArgs &a, const TileShape &p, BackwardLaunch &l) {
     if (a.rms)
-        return p.edge ? launch_backward_tile<T, K, true, WARP, true>(a, p, pg, pb, pdl, stream, launches)
-                      : launch_backward_tile<T, K, false, WARP, true>(a, p, pg, pb, pdl, stream, launches);
-    return p.edge ? launch_backward_tile<T, K, true, WARP, false>(a, p, pg, pb, pdl, stream, launches)
-                  : launch_backward_tile<T, K, false, WARP, false>(a, p, pg, pb, pdl, stream, launches);
+        return p.edge ? launch_backward_tile<T, K, true, WARP, true>(a, p, l)
+                      : launch_backward_tile<T, K, false, WARP, true>(a, p, l);
+    return p.edge ? launch_backward_tile<T, K, true, WARP, false>(a, p, l)
+                  : launch_backward_tile<T, K, false, WARP, false>(a, p, l);
 }
 
-// dgamma (blockIdx.y == 0) and dbeta (1): the sum of `parts` partial rows.  A CTA owns 32
-// columns; its 32 warps take every 32nd partial row each, eight loads in flight, and are
-// joined in shared memory, in order.  shifted: partial row p starts as row p of the matrix
-// does, (mis + p n) mod 8 elements into its first slot.
-constexpr int kJoinColumns = 32;
-constexpr int kJoinThreads = 1024;
-constexpr int kJoinFlight = 8;
-
+// dgamma (blockIdx.y == 0) and dbeta (1): the sum of `parts` partial rows.  A CTA owns
+// 32 * C columns; its warps take every nth partial row each, all their loads in flight at
+// once where there are few enough, and are joined in shared memory, in order.  shifted: column
+// j of partial row p stands where the tile kernel left it, at j + 8 - (the elements from row
+// p's start to the next slot boundary).
 struct JoinArgs {
     const float *part_gamma, *part_beta;
     float *dgamma, *dbeta;
@@ -307,41 +375,55 @@ struct JoinArgs {
     int mis;
     bool shifted;
 };
+constexpr int kJoinFlight = 8;
 
-__global__ void __launch_bounds__(kJoinThreads) mrn_norm_backward_join_kernel(const JoinArgs a) {
-    __shared__ float sums[32][kJoinColumns + 1];
+template <int WARPS, int C>
+__global__ void __launch_bounds__(WARPS * 32) mrn_norm_backward_join_kernel(const JoinArgs a) {
+    __shared__ float sums[WARPS][C * 32];
     pdl_enter();
     const float *part = blockIdx.y == 0 ? a.part_gamma : a.part_beta;
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;
-    const int64_t j = static_cast<int64_t>(blockIdx.x) * kJoinColumns + lane;
-    float s = 0.0f;
-    for (int64_t p0 = warp; p0 < a.parts; p0 += 32 * kJoinFlight) {
-        float v[kJoinFlight];
+    const int64_t j0 = static_cast<int64_t>(blockIdx.x) * (32 * C) + lane;
+    float s[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) s[c] = 0.0f;
+    for (int64_t p0 = warp; p0 < a.parts; p0 += WARPS * kJoinFlight) {
+        float v[kJoinFlight][C];
 #pragma unroll
         for (int i = 0; i < kJoinFlight; ++i) {
-            const int64_t p = p0 + 32 * i;
-            const int64_t off = a.shifted ? (a.mis + p * a.n) & 7 : 0;
-            v[i] = p < a.parts && j < a.n ? part[p * a.stride + off + j] : 0.0f;
+            const int64_t p = p0 + WARPS * i;
+            const int64_t off = a.shifted ? 8 - (-(a.mis + p * a.n) & 7) : 0;
+            const float *from = part + p * a.stride + off + j0;
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                v[i][c] = p < a.parts && j0 + 32 * c < a.n ? from[32 * c] : 0.0f;
         }
 #pragma unroll
-        for (int i = 0; i < kJoinFlight; ++i) s += v[i];
+        for (int i = 0; i < kJoinFlight; ++i)
+#pragma unroll
+            for (int c = 0; c < C; ++c) s[c] += v[i][c];
     }
-    sums[warp][lane] = s;
+#pragma unroll
+    for (int c = 0; c < C; ++c) sums[warp][32 * c + lane] = s[c];
     __syncthreads();
-    // warp c adds up column c: lane w holds warp w's sum
-    const float t = warp_allsum(sums[lane][warp]);
-    const int64_t jc = static_cast<int64_t>(blockIdx.x) * kJoinColumns + warp;
-    if (lane == 0 && jc < a.n) (blockIdx.y == 0 ? a.dgamma : a.dbeta)[jc] = t;
+    for (int c = threadIdx.x; c < 32 * C; c += WARPS * 32) {
+        float t = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) t += sums[w][c];
+        const int64_t j = static_cast<int64_t>(blockIdx.x) * (32 * C) + c;
+        if (j < a.n) (blockIdx.y == 0 ? a.dgamma : a.dbeta)[j] = t;
+    }
 }
 
-cudaError_t launch_join(const JoinArgs &a, bool pdl, cudaStream_t stream, uint64_t *launches) {
-    const int64_t ctas = (a.n + kJoinColumns - 1) / kJoinColumns;
+template <int WARPS, int C>
+cudaError_t launch_join_typed(const JoinArgs &a, bool pdl, cudaStream_t stream, uint64_t *launches) {
+    const int64_t ctas = (a.n + 32 * C - 1) / (32 * C);
     if (ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = dim3(static_cast<unsigned>(ctas), a.dbeta ? 2 : 1, 1);
-    cfg.blockDim = dim3(kJoinThreads, 1, 1);
+    cfg.blockDim = dim3(WARPS * 32, 1, 1);
     cfg.stream = stream;
     if (pdl) {
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -349,9 +431,16 @@ cudaError_t launch_join(const JoinArgs &a, bool pdl, cudaStream_t stream, uint64
         cfg.attrs = attr;
         cfg.numAttrs = 1;
     }
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, mrn_norm_backward_join_kernel, a);
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, mrn_norm_backward_join_kernel<WARPS, C>, a);
     if (err == cudaSuccess) ++*launches;
     return err;
+}
+
+cudaError_t launch_join(const JoinArgs &a, bool pdl, cudaStream_t stream, uint64_t *launches) {
+    // (measured on GB300, us a call: 163840 x 128 bf16, 1216 partial rows, 25.3 with 32 warps
+    // of 32 columns against 27.2 with 16 of 64; 16384 x 4096 bf16 71.2 against 70.0)
+    return a.n <= 1024 ? launch_join_typed<32, 1>(a, pdl, stream, launches)
+                       : launch_join_typed<16, 2>(a, pdl, stream, launches);
 }
 
 template <class T>
@@ -366,37 +455,52 @@ cudaError_t launch_backward_typed(const BackwardArgs &a, int sms, bool pdl, cuda
     if (most == 0) return launch_join(join, pdl, stream, launches);
     const int mis = common_offset(T::kBytes, a.dy, a.x, a.dstream, static_cast<const void *>(a.dx),
                                   static_cast<const void *>(a.dres));
-    TilePlan p = {};
+    BackwardLaunch l = {sms, pdl, stream, launches, most, most, cudaSuccess};
+    bool done = false;
     // (a generator group is a slot only when the operands start on a slot boundary)
     if (mis == 0 || (mis > 0 && a.drop.threshold == 0)) {
-        const TileWish wish = {a.dstream ? 3 : 2, 2, 512, kPartsPerSm};
-        p = plan_tiles(a.rows, a.n, T::kBytes, mis, wish, sms);
+        // Slots per thread for rows of a CTA, and threads of one at most.  Measured on GB300, a
+        // 400 MB call each (us): bf16 n = 4096 2 68.3, 3 68.9; 6656 2 68.3, 4 68.8; 16384 in
+        // clusters of CTAs of 64 threads 4 111, of 128 4 118 and 2 122, of 256 4 131.  f32 n = 4096 3 66.8, 1 69.1; 8192 3 67.6; rmsnorm 4096 x 16384
+        // in clusters 2 (of at most 256 threads) 178, 4 182.
+        const int64_t slots = a.n / 8;
+        int k = T::kBytes == 2 ? (slots <= 1024 ? 2 : 4) : (slots <= 1152 ? 3 : 2);
+        int most_threads = backward_resident(k);
+        if (T::kBytes == 4 && k == 2) most_threads = 256;
+        if (T::kBytes == 2 && k == 4) most_threads = slots <= 2048 ? 64 : (slots <= 4096 ? 128 : 256);
+        //KR
+        const bool few = tile_few_rows(a.rows, a.n, sms);
+        if (few) {
+            k = 1;
+            most_threads = tile_few_threads(a.rows, a.n, sms);
+        }
+        const TileShape p = tile_shape(a.n, mis, k, most_threads, few);
+        if (p.ok && p.warp) {
+            done = p.k == 1   ? launch_backward_k<T, 1, true>(a, p, l)
+                   : p.k == 2 ? launch_backward_k<T, 2, true>(a, p, l)
+                   : p.k == 3 ? launch_backward_k<T, 3, true>(a, p, l)
+                              : launch_backward_k<T, 4, true>(a, p, l);
+        } else if (p.ok) {
+            //MORE
+            constexpr int kOther = T::kBytes == 2 ? 4 : 3;
+            done = k == 1   ? launch_backward_k<T, 1, false>(a, p, l)
+                   : k == 2 ? launch_backward_k<T, 2, false>(a, p, l)
+                            : launch_backward_k<T, kOther, false>(a, p, l);
+        }
+        join.mis = mis;
+        join.shifted = done && p.edge && !p.warp;
     }
-    const int64_t parts = p.ok ? p.ctas / p.cluster : most;
-    if (parts > most) return cudaErrorInvalidConfiguration;   // (the workspace holds `most`)
-    float *pg = a.workspace;
-    float *pb = a.dbeta ? a.workspace + parts * join.stride : nullptr;
-    cudaError_t err;
-    if (p.ok && p.warp) {
-        err = p.k == 1   ? launch_backward_k<T, 1, true>(a, p, pg, pb, pdl, stream, launches)
-              : p.k == 2 ? launch_backward_k<T, 2, true>(a, p, pg, pb, pdl, stream, launches)
-                         : launch_backward_k<T, 4, true>(a, p, pg, pb, pdl, stream, launches);
-    } else if (p.ok) {
-        err = p.k == 1   ? launch_backward_k<T, 1, false>(a, p, pg, pb, pdl, stream, launches)
-              : p.k == 2 ? launch_backward_k<T, 2, false>(a, p, pg, pb, pdl, stream, launches)
-              : p.k == 3 ? launch_backward_k<T, 3, false>(a, p, pg, pb, pdl, stream, launches)
-                         : launch_backward_k<T, 4, false>(a, p, pg, pb, pdl, stream, launches);
-    } else {
+    if (!done) {
         const auto fn = a.rms ? mrn_norm_backward_looped_kernel<T, true>
                               : mrn_norm_backward_looped_kernel<T, false>;
-        err = launch_plain(fn, parts, kLoopedThreads, 0, pdl, stream, launches, a, pg, pb, join.stride);
+        l.parts = most;
+        l.err = launch_plain(fn, most, kLoopedThreads, 0, pdl, stream, launches, a, a.workspace,
+                             a.dbeta ? a.workspace + most * join.stride : nullptr, join.stride);
     }
-    if (err != cudaSuccess) return err;
-    join.part_gamma = pg;
-    join.part_beta = pb;
-    join.parts = parts;
-    join.mis = p.mis;
-    join.shifted = p.ok && p.edge && !p.warp;
+    if (l.err != cudaSuccess) return l.err;
+    join.part_gamma = a.workspace;
+    join.part_beta = a.dbeta ? a.workspace + l.parts * join.stride : nullptr;
+    join.parts = l.parts;
     return launch_join(join, pdl, stream, launches);
 }
 
@@ -405,5 +509,7 @@ cudaError_t launch_norm_backward(bool bf16, const BackwardArgs &a, int sms, bool
     return bf16 ? launch_backward_typed<BF16>(a, sms, pdl, stream, launches)
                 : launch_backward_typed<F32>(a, sms, pdl, stream, launches);
 }
+
+int take_wait_timeouts_norm_backward() { return take_wait_timeouts<kOpBackwardTimeouts>(); }
 
 }  // namespace mrn

@@ -4,12 +4,16 @@
 //
 //  * A thread owns K slots of eight consecutive elements, a row's width in threads
 //    apart.  Slots are cut at multiples of eight elements of the flattened matrix, so
-//    that they are aligned in memory and are the dropout's generator groups; when
-//    the row pitch is not a multiple of eight (EDGE), a row starts `off` elements into
-//    its first slot.  The rows of one CTA are a multiple of eight apart, so `off`
-//    and with it every thread's columns are the same for all of them: weights are
-//    loaded once, and column sums stay in registers over all rows.
-//  * Row operands are copied ahead by cp.async into a ring of `stages` rows in shared
+//    that they are aligned in memory and are the dropout's generator groups.  When the
+//    row pitch is not a multiple of eight (EDGE), up to seven elements before the row's
+//    first whole slot and seven behind its last are taken one by one, each by a lane of
+//    its own: every slot is whole, and only the warp that holds the ends does more.
+//    The rows of one CTA are a multiple of eight apart, so that they all start alike and
+//    a thread's columns stay the same: weights are loaded once, and column sums stay in
+//    registers over all rows.
+//  * R rows at a time: their loads, sums and barriers overlap, and the column sums and
+//    weights are held once for all of them.
+//  * Row operands are copied ahead by cp.async into a ring of `stages` turns in shared
 //    memory, each warp its own columns, so that a stage is handed over by the warp's
 //    own wait and needs no barrier.  The copies in flight cover the latency of the
 //    row sums, whose barriers would otherwise leave the memory idle.
@@ -25,16 +29,18 @@ struct TileArgs {
     int lanes;      // threads per row when several rows share a warp (WARP); else unused
     int stages;     // ring depth
     int mis;        // elements from the slot boundary below the operands' base to the base
+    uint32_t stall; // see row_sum
 };
 
 constexpr int kTileMaxThreads = 512;
-constexpr int tile_max_threads(int k) { return k >= 3 ? 256 : kTileMaxThreads; }
 constexpr int kTileMaxStages = 4;
 constexpr int kTileMaxOperands = 3;
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;"
-                 :: "r"(dst), "l"(src) : "memory");
+// 16 bytes to shared memory when `on` is not 0 (predicated, no branch).
+__device__ __forceinline__ void cp_async16_if(uint32_t on, uint32_t dst, const void *src) {
+    asm volatile("{.reg .pred q; setp.ne.u32 q, %2, 0;"
+                 " @q cp.async.cg.shared.global.L2::256B [%0], [%1], 16;}"
+                 :: "r"(dst), "l"(src), "r"(on) : "memory");
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(dst), "l"(src) : "memory");
@@ -63,52 +69,102 @@ __device__ __forceinline__ void ld_shared_slot(Slot<F32> &s, uint32_t p) {
 }
 
 // Sums of N values over the threads of a row.  WARP: over `width` lanes; else over
-// the CTA and, for rows split over a cluster, over its CTAs.
+// the CTA and, for rows split over a cluster, over its CTAs: every CTA sends its sums to
+// every peer as st.async messages, which land in the peer's box for this turn and complete
+// the peer's mbarrier for it; a CTA waits for its own and adds the sums in rank order (all
+// CTAs get the same bits).  A cluster barrier instead would make each row wait for the
+// stores of the row before it (16384 f32: 193 us against %CLUSTER% us for the gradient of
+// 4096 rows).  Boxes and mbarriers alternate: a CTA sends turn t + 2 only after it has every
+// peer's t + 1, which a peer sends only after all its threads have read t.
 template <int N> struct RowSumSlots {
     CtaSumSlots<N> cta;
-    float peer[2][N][kMaxCluster];
+    float box[2][N][kMaxCluster];   // [turn parity][value][sender rank]
+    __align__(8) uint64_t bar[2];
 };
 
+// Before the first row_sum of a cluster, by every thread: every peer's mbarriers are set up.
+template <int N> __device__ __forceinline__ void row_sum_setup(RowSumSlots<N> &s, unsigned cl) {
+    if (cl > 1) {
+        if (threadIdx.x == 0) {
+            mbar_init(&s.bar[0], 1);
+            mbar_init(&s.bar[1], 1);
+            fence_mbar_init();
+        }
+        __syncthreads();
+        cluster_arrive_release();
+    }
+}
+__device__ __forceinline__ void row_sum_ready(unsigned cl) {
+    if (cl > 1) cluster_wait_acquire();
+}
+// After the last: no CTA leaves while a peer may still send to it.
+__device__ __forceinline__ void row_sum_leave(unsigned cl) {
+    if (cl > 1) {
+        cluster_arrive_release();
+        cluster_wait_acquire();
+    }
+}
+
+// False (in the whole CTA) when a peer's message did not arrive in time (about a second): the
+// CTA then stops, and its peers after it.  `stall`: bytes more than ever arrive that a wait
+// expects (a test hook, 0 in use).
 template <int N, bool WARP>
-__device__ __forceinline__ void row_sum(float (&v)[N], RowSumSlots<N> &s, int &turn, int width,
-                                        unsigned cl, unsigned crank) {
+__device__ __forceinline__ bool row_sum(float (&v)[N], RowSumSlots<N> &s, int &turn, int width,
+                                        unsigned cl, unsigned crank, uint32_t stall) {
     if constexpr (WARP) {
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] = group_allsum(v[i], width);
     } else {
         cta_sum(v, s.cta, turn);
         if (cl > 1) {
-            // (two turns: a peer writes turn t + 2 after the barrier of t + 1, which this
-            // CTA enters after its reads of t)
+            const int p = turn & 1;
             const unsigned lane = threadIdx.x & 31;
-            if (threadIdx.x < cl) {
+            if (threadIdx.x == 0) mbar_arrive_expect_tx(&s.bar[p], (cl - 1) * 4u * N + stall);
+            if (threadIdx.x < cl && threadIdx.x != crank) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) st_cluster_f32(&s.peer[turn][i][crank], threadIdx.x, v[i]);
+                for (int i = 0; i < N; ++i) send_f32(&s.box[p][i][crank], &s.bar[p], threadIdx.x, v[i]);
             }
-            cluster_arrive_release();
-            cluster_wait_acquire();
+            const bool late = !mbar_wait_bounded_cluster(&s.bar[p], static_cast<uint32_t>((turn - 1) >> 1 & 1));
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = warp_allsum(lane < cl ? s.peer[turn][i][lane] : 0.0f);
+            for (int i = 0; i < N; ++i)
+                v[i] = warp_allsum(lane >= cl ? 0.0f : (lane == crank ? v[i] : s.box[p][i][lane]));
+            if (__syncthreads_or(late)) {
+                if (threadIdx.x == 0) atomicAdd(&g_wait_timeouts, 1u);
+                return false;
+            }
         }
     }
+    return true;
 }
 
-template <class T, int K, bool EDGE, bool WARP> struct RowTile {
+// The single elements at a row's ends in the ring: one word per lane that holds one (bf16: the
+// word that holds the element).
+constexpr int kEndLanes = 16;    // lanes 0..6 the ones before the slots, 8..14 the ones behind
+template <int OPS, int R, bool EDGE, bool WARP> struct EndSlots {
+    static constexpr int kThreads = !EDGE ? 1 : (WARP ? 128 : kEndLanes);
+    uint32_t w[kTileMaxStages][R][OPS][kThreads];
+};
+
+template <class T, int K, int R, bool EDGE, bool WARP> struct RowTile {
     static constexpr int kChunks = T::kBytes / 2;          // 16-byte chunks per slot
     static constexpr int kChunkElems = 8 / kChunks;
 
     int width;            // threads per row (in this CTA)
     int first;            // this thread's first slot; slot k is first + k * width
-    int off;              // elements of the row's first slot that precede the row
+    int before;           // EDGE: elements from the row's start to the next slot boundary
     unsigned cl, crank;
-    int64_t n, rows;
-    int64_t row;          // this thread's row; the next is row + stride
+    int64_t row;          // this thread's first row; the R rows are `stride` apart
     int64_t stride;
+    int left;             // rows from this one on that exist
+    int cta_left;         // ... of the CTA's first row: uniform, so that all threads of a CTA
+                          // make the same number of turns
     int64_t at;           // byte offset of the row's slot 0 from the slot boundary below its operand
     int64_t step;         // bytes to the next row's
     int team;             // index in the CTA of the lanes that copy together
     bool leads;           // the first of them
-    uint32_t in[K];       // elements of slot k inside the row: bit i for element i
+    bool ends;            // EDGE: this warp holds single elements (uniform over the warp)
+    int end_col;          // column of this thread's single element; -1: none
+    uint32_t full;        // slots of this thread inside the row: bit k
     uint32_t copies;      // chunks this thread copies: bit k * kChunks + c
     uint32_t region;      // bytes of one slot index k of all threads in the ring
     uint32_t copy_base;   // this thread's place in a region: as copier,
@@ -116,8 +172,7 @@ template <class T, int K, bool EDGE, bool WARP> struct RowTile {
     int copy_off;         // byte offset in the row of the first chunk this thread copies
     int copy_step;        // ... and from chunk to chunk of a slot
 
-    __device__ __forceinline__ RowTile(int64_t rows_, int64_t n_, const TileArgs &t)
-        : n(n_), rows(rows_) {
+    __device__ __forceinline__ RowTile(int64_t rows, int64_t n, const TileArgs &t) {
         const int tid = threadIdx.x, lane = tid & 31;
         int lanes = 32, li = lane;      // lanes that copy together, and this one's index
         team = tid >> 5;
@@ -141,47 +196,51 @@ template <class T, int K, bool EDGE, bool WARP> struct RowTile {
             stride = gridDim.x / cl;
         }
         leads = li == 0;
+        const int64_t cta_row = WARP ? row - team : row;
+        left = row < rows ? static_cast<int>((rows - 1 - row) / stride) + 1 : 0;
+        cta_left = cta_row < rows ? static_cast<int>((rows - 1 - cta_row) / stride) + 1 : 0;
         const int64_t e0 = t.mis + row * n;
-        off = EDGE ? static_cast<int>(e0 & 7) : 0;
-        at = (e0 - off) * T::kBytes;
+        before = EDGE ? static_cast<int>(-e0 & 7) : 0;
+        at = (e0 + before) * T::kBytes;
         step = stride * n * T::kBytes;
+        const int head = before < n ? before : static_cast<int>(n);
+        const int slots = static_cast<int>((n - head) / 8);
+        ends = EDGE && (WARP || (tid < 32 && crank == 0));
+        end_col = -1;
+        if (ends) {
+            const int j = WARP ? first : tid;
+            if (j < 8) {
+                if (j < head) end_col = j;
+            } else if (j < kEndLanes) {
+                const int64_t c = head + slots * int64_t(8) + (j - 8);
+                if (c < n) end_col = static_cast<int>(c);
+            }
+        }
         region = blockDim.x * kChunks * 16;
-        const int chunk0 = (first - li) * 8 + li * kChunkElems;     // element in the slot row
-        copy_off = chunk0 * T::kBytes;
+        const int chunk0 = (first - li) * kChunks + li;             // chunk in the slot row
+        copy_off = chunk0 * 16;
         copy_step = lanes * 16;
         copy_base = static_cast<uint32_t>(((tid - li) * kChunks + li) * 16);
         slot_base = static_cast<uint32_t>(tid * kChunks * 16);
-        copies = 0u;
+        full = copies = 0u;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int64_t j = column(k);
-            uint32_t m = 0xFFu;
-            if (j < 0) m &= 0xFFu << static_cast<int>(-j);
-            if (j + 8 > n) m = j < n ? m & (0xFFu >> static_cast<int>(j + 8 - n)) : 0u;
-            in[k] = m;
+            if (first + k * width < slots) full |= 1u << k;
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-                const int64_t jc = chunk0 + k * width * 8 + c * lanes * kChunkElems - off;
-                if (jc < n && jc + kChunkElems > 0) copies |= 1u << (k * kChunks + c);
-            }
+            for (int c = 0; c < kChunks; ++c)
+                if (chunk0 + k * width * kChunks + c * lanes < slots * kChunks)
+                    copies |= 1u << (k * kChunks + c);
         }
     }
-
-    // First row of this CTA's iteration: uniform over the CTA, so that all its threads
-    // make the same number of iterations.
-    __device__ __forceinline__ int64_t cta_row() const {
-        if constexpr (WARP) {
-            return row - team;
-        } else {
-            return row;
-        }
-    }
-    __device__ __forceinline__ int column(int k) const { return (first + k * width) * 8 - off; }
+    __device__ __forceinline__ bool valid(int rr) const { return rr < left; }
+    __device__ __forceinline__ bool holds(int k) const { return (full >> k) & 1u; }
+    // First column of slot k.
+    __device__ __forceinline__ int column(int k) const { return (first + k * width) * 8 + before; }
 
     // Zeroes a ring of `stages` stages of `count` operands: the chunks outside the row are
     // never copied, and read as zeros ever after.
     __device__ __forceinline__ void clear(uint32_t ring, int stages, int count) const {
-        for (int i = 0; i < stages * count * K; ++i) {
+        for (int i = 0; i < stages * R * count * K; ++i) {
 #pragma unroll
             for (int c = 0; c < kChunks; ++c)
                 asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};"
@@ -189,66 +248,89 @@ template <class T, int K, bool EDGE, bool WARP> struct RowTile {
         }
         __syncwarp();
     }
-    // Copies the row `ahead` rows from this one into the ring's stage at `to` (one group of
-    // asynchronous copies with what was issued since the last).
-    __device__ __forceinline__ void issue(uint32_t to, int ahead, const char *const (&ops)[kTileMaxOperands],
-                                          int count) const {
-        if (row + ahead * stride < rows) {
-            const int64_t from = at + ahead * step + copy_off;
+    // Copies the rows `turns` turns of R rows from these into the ring's stage at `to` (and
+    // the single elements to end_w[stage]), as one group of asynchronous copies with what was
+    // issued since the last.
+    template <int OPS, class Ends>
+    __device__ __forceinline__ void issue(uint32_t to, int stage, int turns, const char *const (&ops)[OPS],
+                                          int count, Ends &end_w) const {
 #pragma unroll
-            for (int o = 0; o < kTileMaxOperands; ++o) {
-                if (o >= count) break;
-                const char *src = ops[o] + from;
-                const uint32_t dst = to + o * K * region + copy_base;
+        for (int rr = 0; rr < R; ++rr) {
+            if (turns * R + rr < left) {
+                const int64_t row_at = at + (turns * R + rr) * step;
 #pragma unroll
-                for (int k = 0; k < K; ++k) {
+                for (int o = 0; o < OPS; ++o) {
+                    if (o >= count) break;
+                    const char *src = ops[o] + (row_at + copy_off);
+                    const uint32_t dst = to + (rr * count + o) * K * region + copy_base;
 #pragma unroll
-                    for (int c = 0; c < kChunks; ++c) {
-                        if ((copies >> (k * kChunks + c)) & 1u)
-                            cp_async16(dst + k * region + c * copy_step,
-                                       src + k * (width * 8 * T::kBytes) + c * copy_step);
+                    for (int k = 0; k < K; ++k) {
+#pragma unroll
+                        for (int c = 0; c < kChunks; ++c)
+                            cp_async16_if(copies & (1u << (k * kChunks + c)), dst + k * region + c * copy_step,
+                                          src + k * (width * 8 * T::kBytes) + c * copy_step);
+                    }
+                }
+                if (EDGE && ends) {
+                    if (end_col >= 0) {
+                        const int64_t e = row_at + (end_col - before) * T::kBytes;
+#pragma unroll
+                        for (int o = 0; o < OPS; ++o) {
+                            if (o >= count) break;
+                            cp_async4(static_cast<uint32_t>(__cvta_generic_to_shared(
+                                          &end_w.w[stage][rr][o][threadIdx.x])),
+                                      ops[o] + (e & ~int64_t(3)));
+                        }
                     }
                 }
             }
         }
         cp_async_commit();
     }
-    // This thread's slots of operand o in the stage at `from`, zero outside the row.
-    __device__ __forceinline__ void fetch(Slot<T> (&s)[K], uint32_t from, int o) const {
-        const uint32_t src = from + o * K * region + slot_base;
+    // This thread's slots of operand o of row rr in the stage at `from`, zero outside the row.
+    __device__ __forceinline__ void fetch(Slot<T> (&s)[K], uint32_t from, int o, int rr, int count) const {
+        const uint32_t src = from + (rr * count + o) * K * region + slot_base;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            ld_shared_slot(s[k], src + k * region);
-            if constexpr (EDGE) {
-                if (in[k] != 0xFFu && in[k] != 0u) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (!((in[k] >> i) & 1u)) s[k].clear(i);
-                }
-            }
-        }
-        if constexpr (WARP) {
-            if (row >= rows) {      // (past the last row: the stage holds an earlier one)
+        for (int k = 0; k < K; ++k) ld_shared_slot(s[k], src + k * region);
+        if constexpr (WARP || R > 1) {
+            if (!valid(rr)) {      // (past the last row: the stage holds an earlier one)
 #pragma unroll
                 for (int k = 0; k < K; ++k) s[k].zero();
             }
         }
     }
-    // Stores slot k of this row (the elements inside it) at `base`, the slot boundary below
-    // the operand's first element.
-    __device__ __forceinline__ void store(char *base, int k, const Slot<T> &s) const {
-        char *p = base + at + (first + k * width) * (8 * T::kBytes);
-        if (!EDGE || in[k] == 0xFFu) {
-            if (in[k] != 0u) st_slot(p, s);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if ((in[k] >> i) & 1u) s.st_one(p + i * T::kBytes, i);
-        }
+    // This thread's single element of operand o; 0 when it has none.
+    template <class Ends>
+    __device__ __forceinline__ float fetch_end(const Ends &end_w, int stage, int o, int rr) const {
+        if (end_col < 0 || !valid(rr)) return 0.0f;
+        const uint32_t w = end_w.w[stage][rr][o][threadIdx.x];
+        if constexpr (T::kBytes == 4) return __uint_as_float(w);
+        const bool high = ((at >> 1) + end_col - before) & 1;
+        return __uint_as_float(high ? w & 0xFFFF0000u : w << 16);
     }
-    // Generator group of slot k (the operands start on a slot boundary).
-    __device__ __forceinline__ uint64_t group(int k) const {
-        return static_cast<uint64_t>(at) / (8 * T::kBytes) + static_cast<uint64_t>(first + k * width);
+    // Stores the slots of row rr (if `on`) at `base`, the slot boundary below the operand's
+    // first element.
+    __device__ __forceinline__ void store(char *base, int rr, bool on, const Slot<T> (&s)[K]) const {
+        char *p = base + at + rr * step + first * (8 * T::kBytes);
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            st_slot_if(on && holds(k), p + k * (width * 8 * T::kBytes), s[k]);
+    }
+    // Stores this thread's single element; returns it as stored.
+    __device__ __forceinline__ float store_end(char *base, int rr, bool on, float v) const {
+        Frag<T, 1> f;
+        const float o[1] = {v};
+        f.put(o);
+        if (on && end_col >= 0) st_global(base + at + rr * step + (end_col - before) * T::kBytes, f);
+        return f.get(0);
+    }
+    // Generator group of slot k (the operands start on a slot boundary), and the element number
+    // of the single element.
+    __device__ __forceinline__ uint64_t group(int rr, int k) const {
+        return static_cast<uint64_t>(at + rr * step) / (8 * T::kBytes) + static_cast<uint64_t>(first + k * width);
+    }
+    __device__ __forceinline__ int64_t end_element(int rr) const {
+        return (at + rr * step) / T::kBytes + end_col - before;
     }
     // The thread's columns of a weight vector, zeros outside the row; once per CTA.  All
     // loads are independent of each other.
@@ -256,36 +338,43 @@ template <class T, int K, bool EDGE, bool WARP> struct RowTile {
         const bool whole = !EDGE && reinterpret_cast<uintptr_t>(w) % 16 == 0;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int64_t j = column(k);
+            const int64_t j = holds(k) ? column(k) : 0;
+            s[k].zero();
             if (whole) {
-                const int64_t jj = in[k] ? j : 0;
+                if (holds(k)) {
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c)
-                    asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];"
-                                 : "=r"(s[k].w[4 * c]), "=r"(s[k].w[4 * c + 1]),
-                                   "=r"(s[k].w[4 * c + 2]), "=r"(s[k].w[4 * c + 3])
-                                 : "l"(elem_ptr<T>(w, jj) + c * 16));
-                if (!in[k]) s[k].zero();
-            } else {
+                    for (int c = 0; c < kChunks; ++c)
+                        asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                     : "=r"(s[k].w[4 * c]), "=r"(s[k].w[4 * c + 1]),
+                                       "=r"(s[k].w[4 * c + 2]), "=r"(s[k].w[4 * c + 3])
+                                     : "l"(elem_ptr<T>(w, j) + c * 16));
+                }
+            } else if (holds(k)) {
                 Frag<T, 1> f[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ld_ro(f[i], elem_ptr<T>(w, ((in[k] >> i) & 1u) ? j + i : 0));
-                s[k].zero();
+                for (int i = 0; i < 8; ++i) ld_ro(f[i], elem_ptr<T>(w, j + i));
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     if constexpr (T::kBytes == 4) {
-                        s[k].w[i] = ((in[k] >> i) & 1u) ? f[i].w : 0u;
+                        s[k].w[i] = f[i].w;
                     } else {
-                        if ((in[k] >> i) & 1u)
-                            s[k].w[i >> 1] |= static_cast<uint32_t>(f[i].h) << ((i & 1) * 16);
+                        s[k].w[i >> 1] |= static_cast<uint32_t>(f[i].h) << ((i & 1) * 16);
                     }
                 }
             }
         }
     }
+    __device__ __forceinline__ float end_weight(const void *w) const {
+        if (end_col < 0) return 0.0f;
+        Frag<T, 1> f;
+        ld_ro(f, elem_ptr<T>(w, end_col));
+        return f.get(0);
+    }
     __device__ __forceinline__ void advance() {
-        row += stride;
-        at += step;
+        row += R * stride;
+        at += R * step;
+        left -= R;
+        cta_left -= R;
     }
 };
 
@@ -302,8 +391,10 @@ struct RingWalk {
     }
 };
 
+// Static shared memory of a tile kernel at most.
+constexpr int64_t kTileStaticShared = 12288;
 // Dynamic shared memory that a ring may use: the rest is the static row-sum slots.
-constexpr int64_t kTileSharedBudget = kSharedBytesPerCta - 8192;
+constexpr int64_t kTileSharedBudget = kSharedBytesPerCta - kTileStaticShared;
 
 // Dynamic shared memory of a ring.
 inline int64_t tile_ring_bytes(int elem_bytes, int k, int threads, int stages, int operands) {
@@ -311,61 +402,89 @@ inline int64_t tile_ring_bytes(int elem_bytes, int k, int threads, int stages, i
 }
 
 // How a call's rows are laid over threads.
-struct TilePlan {
+struct TileShape {
     bool ok;          // false: the looped kernel
     bool warp;        // several rows per warp
     bool edge;
-    int k, threads, lanes, cluster, stages;
-    int64_t ctas;
+    int k, threads, lanes, cluster;
     int mis;
 };
 
-struct TileWish {
-    int operands;          // row operands copied ahead
-    int slots_per_thread;  // for rows of a CTA
-    int threads_per_sm;    // resident threads to aim for
-    int most_ctas_per_sm;
+constexpr int kWarpTileThreads = 128;
+constexpr int kWarpTileSlots = 128;    // rows of at most this many slots share warps
+
+// Few rows, at most one per SM, of more slots than a warp's: what counts is how soon one row is
+// done.  One slot per thread, and a row of 512 slots or more over as many CTAs of 64
+// threads or more as there are SMs for it (measured on GB300, us a call: layernorm 1 x 6656
+// f32 2.7 against 3.2 in one CTA of 416 threads, its gradient 4.0 against 6.0; the gradient of
+// 64 x 768 f32 4.2 against 5.1 in warps).
+inline bool tile_few_rows(int64_t rows, int64_t n, int sms) {
+    return rows <= sms && n / 8 > 32 && n / 8 <= int64_t(kMaxCluster) * 512;
+}
+inline int tile_few_threads(int64_t rows, int64_t n, int sms) {
+    const int64_t slots = n / 8;
+    int threads = 64;
+    while (threads < 512 && (slots < 512 || rows * ((slots + threads - 1) / threads) > sms ||
+                             (slots + threads - 1) / threads > kMaxCluster))
+        threads *= 2;
+    return threads;
+}
+
+// Shape of rows of n elements whose operands lie `mis` elements past a slot boundary:
+// `k` slots per thread for rows of a CTA, CTAs of at most `most_threads`.
+inline TileShape tile_shape(int64_t n, int mis, int k, int most_threads, bool few) {
+    TileShape s = {};
+    s.mis = mis;
+    s.edge = mis != 0 || n % 8 != 0;
+    s.cluster = 1;
+    s.lanes = 32;
+    const int64_t slots = n < 8 ? 1 : n / 8;
+    if (slots <= kWarpTileSlots && !few) {
+        s.warp = true;
+        s.k = slots <= 8 ? 1 : (slots <= 64 ? 2 : (slots <= 96 ? 3 : 4));
+        s.lanes = s.edge ? kEndLanes : 1;      // (a lane for each element at the ends)
+        while (s.lanes * s.k < slots) s.lanes *= 2;
+        s.threads = kWarpTileThreads;
+    } else {
+        s.k = k;
+        const int64_t most = int64_t(k) * most_threads;
+        s.cluster = static_cast<int>((slots + most - 1) / most);
+        if (s.cluster > kMaxCluster) return s;
+        const int64_t per = (slots + s.cluster - 1) / s.cluster;
+        s.threads = static_cast<int>((per + 32 * k - 1) / (32 * k)) * 32;
+    }
+    s.ok = true;
+    return s;
+}
+
+// The rest of a launch: as many CTAs as the registers let an SM hold, a ring as deep as
+// shared memory then allows (two stages at least where it can be), and a persistent grid.
+struct TileGrid {
+    int stages;       // 0: the ring does not fit
+    int64_t ctas;
 };
 
-inline TilePlan plan_tiles(int64_t rows, int64_t n, int elem_bytes, int mis, const TileWish &wish,
-                           int sms) {
-    TilePlan p = {};
-    p.mis = mis;
-    p.edge = mis != 0 || n % 8 != 0;
-    p.cluster = 1;
-    const int64_t slots = p.edge ? (n + 14) / 8 : n / 8;
-    if (slots <= 128) {
-        p.warp = true;
-        p.k = slots <= 8 ? 1 : (slots <= 64 ? 2 : 4);
-        p.lanes = 1;
-        while (p.lanes * p.k < slots) p.lanes *= 2;
-        p.threads = 128;
-    } else {
-        p.k = wish.slots_per_thread;
-        const int64_t most = int64_t(p.k) * tile_max_threads(p.k);
-        p.cluster = static_cast<int>((slots + most - 1) / most);
-        if (p.cluster > kMaxCluster) return p;
-        const int64_t per = (slots + p.cluster - 1) / p.cluster;
-        p.threads = static_cast<int>((per + 32 * p.k - 1) / (32 * p.k)) * 32;
+inline TileGrid tile_grid(const TileShape &s, int64_t rows, int rows_at_a_time, int elem_bytes, int operands,
+                          int resident, int most_ctas_per_sm, int sms) {
+    TileGrid g = {};
+    int per_sm = resident < most_ctas_per_sm ? resident : most_ctas_per_sm;
+    const int64_t stage = tile_ring_bytes(elem_bytes, s.k, s.threads, 1, operands * rows_at_a_time);
+    for (;; --per_sm) {
+        const int64_t budget = (kTileSharedBudget - (per_sm - 1) * kTileStaticShared) / per_sm;
+        g.stages = static_cast<int>(budget / stage);
+        if (g.stages >= 2 || per_sm == 1) break;
     }
-    const int64_t stage = tile_ring_bytes(elem_bytes, p.k, p.threads, 1, wish.operands);
-    int64_t per_sm = wish.threads_per_sm / p.threads;
-    if (per_sm > wish.most_ctas_per_sm) per_sm = wish.most_ctas_per_sm;
-    if (per_sm < 1) per_sm = 1;
-    const int64_t budget = (kTileSharedBudget - (per_sm - 1) * 8192) / per_sm;
-    p.stages = static_cast<int>(budget / stage);
-    if (p.stages > kTileMaxStages) p.stages = kTileMaxStages;
-    if (p.stages < 1) return p;
     //TUNE
-    const int64_t rows_per_cta = p.warp ? p.threads / p.lanes : 1;
-    int64_t groups = sms * per_sm / p.cluster;      // CTAs or clusters
-    if (groups * rows_per_cta % 8 != 0 && groups > 8) groups -= groups % 8;
+    if (g.stages > kTileMaxStages) g.stages = kTileMaxStages;
+    const int64_t rows_per_cta = s.warp ? s.threads / s.lanes : 1;
+    int64_t groups = static_cast<int64_t>(sms) * per_sm / s.cluster;      // CTAs or clusters
+    // rows of one CTA start alike only when they are a multiple of eight apart
+    if (groups > 8) groups -= groups % 8;
     if (groups < 8) groups = 8;
     const int64_t need = (rows + rows_per_cta - 1) / rows_per_cta;
     if (groups > need) groups = need;
-    p.ctas = groups * p.cluster;
-    p.ok = true;
-    return p;
+    g.ctas = groups * s.cluster;
+    return g;
 }
 
 // Elements from the slot boundary below a row operand to its base; -1 when the
@@ -378,20 +497,24 @@ template <class... P> inline int common_offset(int elem_bytes, const void *first
     return static_cast<int>(at) / elem_bytes;
 }
 
-// Which kernels have been opened to the shared memory and cluster sizes below, per
-// device.  Every thread sets the same values, so that calls that race only repeat them.
+// What is known of a kernel on each device: the CTAs that an SM's registers hold at the
+// last number of threads asked for (threads * 64 + CTAs; 0 until the kernel has been opened to
+// the shared memory and the cluster sizes below).  Every thread finds the same values, so
+// that calls that race only repeat them.
 struct TileLaunchCache {
-    std::atomic<bool> opened[kMaxCachedDevices];
+    std::atomic<int> resident[kMaxCachedDevices];
 };
 
-template <class... Params, class... Args>
-cudaError_t launch_tile(TileLaunchCache &cache, void (*fn)(Params...), const TilePlan &p, int64_t shared,
-                        bool pdl, cudaStream_t stream, uint64_t *launches, Args... args) {
+template <class... Params>
+cudaError_t open_tile(TileLaunchCache &cache, void (*fn)(Params...), int threads, int *resident) {
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
     const bool cached = dev >= 0 && dev < kMaxCachedDevices;
-    if (!cached || !cache.opened[dev].load(std::memory_order_relaxed)) {
+    const int known = cached ? cache.resident[dev].load(std::memory_order_acquire) : 0;
+    *resident = known % 64;
+    if (known / 64 == threads) return cudaSuccess;
+    if (known == 0) {
         err = cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    static_cast<int>(kTileSharedBudget));
@@ -399,11 +522,21 @@ cudaError_t launch_tile(TileLaunchCache &cache, void (*fn)(Params...), const Til
         err = cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
                                    cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (err != cudaSuccess) return err;
-        if (cached) cache.opened[dev].store(true, std::memory_order_relaxed);
     }
+    err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(resident, fn, threads, 0);
+    if (err != cudaSuccess) return err;
+    if (*resident < 1) return cudaErrorInvalidConfiguration;
+    if (cached) cache.resident[dev].store(threads * 64 + *resident, std::memory_order_release);
+    return cudaSuccess;
+}
+
+template <class... Params, class... Args>
+cudaError_t launch_tile(void (*fn)(Params...), const TileShape &p, int64_t ctas, int64_t shared, bool pdl,
+                        cudaStream_t stream, uint64_t *launches, Args... args) {
+    if (ctas < 1 || ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
-    cfg.gridDim = dim3(static_cast<unsigned>(p.ctas), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
     cfg.blockDim = dim3(static_cast<unsigned>(p.threads), 1, 1);
     cfg.dynamicSmemBytes = static_cast<size_t>(shared);
     cfg.stream = stream;
@@ -420,7 +553,7 @@ cudaError_t launch_tile(TileLaunchCache &cache, void (*fn)(Params...), const Til
         attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
         ++cfg.numAttrs;
     }
-    err = cudaLaunchKernelEx(&cfg, fn, args...);
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, fn, args...);
     if (err == cudaSuccess) ++*launches;
     return err;
 }

@@ -32,6 +32,7 @@ struct LayernormArgs {
     DropArgs drop;
     int64_t rows, n;
     float eps;
+    uint32_t stall;             // bytes that a cluster's first wait expects in vain (test hook)
 };
 
 // The gradient of LayerNorm (rms false) or RMSNorm (rms true) at x.
@@ -48,6 +49,7 @@ struct BackwardArgs {
     DropArgs drop;
     int64_t rows, n;
     float eps;                  // RMSNorm
+    uint32_t stall;             // as above
     bool rms;
 };
 
@@ -66,11 +68,17 @@ cudaError_t launch_norm_backward(bool bf16, const BackwardArgs &a, int sms, bool
 cudaError_t launch_dropout(bool bf16, const DropoutArgs &a, bool pdl, cudaStream_t stream,
                            uint64_t *launches);
 
+// Bounded waits of these kernels' clusters that ran out since the last call; the tags keep the
+// counters of the two apart from each other's and the operations'.
+enum { kOpLayernormTimeouts = 100, kOpBackwardTimeouts = 101 };
+int take_wait_timeouts_layernorm();
+int take_wait_timeouts_norm_backward();
+
 // Partial sums of dgamma (and of dbeta) that a backward pass keeps at most: the
 // rows of [parts x part_stride_of(n)] floats in its workspace, for each of the two.
 int64_t backward_parts(int64_t rows, int64_t n, int sms);
-// Floats from one partial row to the next: whole slots of eight for a row that may
-// start anywhere in one.
-constexpr int64_t part_stride_of(int64_t n) { return (n + 14) / 8 * 8; }
+// Floats from one partial row to the next: whole slots of eight, and up to seven elements
+// before them.
+constexpr int64_t part_stride_of(int64_t n) { return (n + 15) / 8 * 8; }
 
 }  // namespace mrn

@@ -112,6 +112,7 @@ mrn_status backward(BackwardCall &c, cudaStream_t stream) {
     st = b.check();
     if (st != MRN_OK) return st;
     if (c.workspace_bytes < needed) return MRN_ERR_INVALID_SIZE;
+    a.stall = launch_stall_bytes();
     a.workspace = static_cast<float *>(const_cast<void *>(c.workspace));
     uint64_t launched = 0;
     const cudaError_t err = launch_norm_backward(c.dtype == MRN_BF16, a, sm_count_of_current_device(),
@@ -119,7 +120,7 @@ mrn_status backward(BackwardCall &c, cudaStream_t stream) {
     return launch_result(err, launched);
 }
 
-mrn_status layernorm(const LayernormArgs &a, bool add, mrn_dtype dtype, cudaStream_t stream) {
+mrn_status layernorm(LayernormArgs &a, bool add, mrn_dtype dtype, cudaStream_t stream) {
     mrn_status st = check_common(a.rows, a.n, dtype, a.eps, a.eps);
     if (st != MRN_OK || a.rows == 0) return st;
     Buffers b;
@@ -138,6 +139,7 @@ mrn_status layernorm(const LayernormArgs &a, bool add, mrn_dtype dtype, cudaStre
     b.add(kOut, a.rstd, a.rows * 4, 4, a.mean == nullptr);
     st = b.check();
     if (st != MRN_OK) return st;
+    a.stall = launch_stall_bytes();
     uint64_t launched = 0;
     const cudaError_t err = launch_layernorm(dtype == MRN_BF16, a, sm_count_of_current_device(),
                                              launch_pdl(), stream, &launched);

@@ -116,31 +116,55 @@ __device__ __forceinline__ void cta_sum(float (&v)[1], CtaSumSlots<1> &s, int &t
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;
     const int nwarps = blockDim.x >> 5;
-    turn ^= 1;
+    const int p = ++turn & 1;
     v[0] = warp_allsum(v[0]);
-    if (lane == 0) s.v[turn][0][warp] = v[0];
+    if (lane == 0) s.v[p][0][warp] = v[0];
     __syncthreads();
-    v[0] = warp_allsum(lane < nwarps ? s.v[turn][0][lane] : 0.0f);
+    v[0] = warp_allsum(lane < nwarps ? s.v[p][0][lane] : 0.0f);
 }
 
-// Two values at once (at most 16 warps): the first exchange leaves one value with each half
-// of the warp, so that both take little more than the shuffles of one.
+// Two and four values at once (at most 16 warps): the first exchanges leave one value with
+// each half or quarter of the warp, so that all of them take little more than the shuffles
+// of one.
 __device__ __forceinline__ void cta_sum(float (&v)[2], CtaSumSlots<2> &s, int &turn) {
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;
     const int nwarps = blockDim.x >> 5;
     const int half = lane >> 4;
-    turn ^= 1;
+    const int p = ++turn & 1;
     float t = (half ? v[1] : v[0]) + __shfl_xor_sync(0xFFFFFFFFu, half ? v[0] : v[1], 16);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
-    if ((lane & 15) == 0) s.v[turn][half][warp] = t;
+    if ((lane & 15) == 0) s.v[p][half][warp] = t;
     __syncthreads();
-    t = (lane & 15) < nwarps ? s.v[turn][half][lane & 15] : 0.0f;
+    t = (lane & 15) < nwarps ? s.v[p][half][lane & 15] : 0.0f;
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
     v[0] = __shfl_sync(0xFFFFFFFFu, t, 0);
     v[1] = __shfl_sync(0xFFFFFFFFu, t, 16);
+}
+
+__device__ __forceinline__ void cta_sum(float (&v)[4], CtaSumSlots<4> &s, int &turn) {
+    const int lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5;
+    const int nwarps = blockDim.x >> 5;
+    const int quarter = lane >> 3, upper = lane >> 4, odd = quarter & 1;
+    const int p = ++turn & 1;
+    // the upper half of the warp keeps values 2 and 3, the lower 0 and 1
+    const float a = (upper ? v[2] : v[0]) + __shfl_xor_sync(0xFFFFFFFFu, upper ? v[0] : v[2], 16);
+    const float b = (upper ? v[3] : v[1]) + __shfl_xor_sync(0xFFFFFFFFu, upper ? v[1] : v[3], 16);
+    float t = (odd ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 8);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+    if ((lane & 7) == 0) s.v[p][quarter][warp] = t;
+    __syncthreads();
+    const int w = lane & 7;
+    t = (w < nwarps ? s.v[p][quarter][w] : 0.0f) +
+        (w + 8 < nwarps ? s.v[p][quarter][w + 8] : 0.0f);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, t, 8 * i);
 }
 
 // One kernel launch with the library's programmatic dependent launch option.
@@ -214,13 +238,16 @@ template <class T> struct Slot {
             w[i >> 1] &= (i & 1) ? 0x0000FFFFu : 0xFFFF0000u;
         }
     }
-    __device__ __forceinline__ void st_one(char *p, int i) const {
+    // element i alone at p, when `on` is not 0 (a predicated store, no branch)
+    __device__ __forceinline__ void st_one_if(char *p, int i, uint32_t on) const {
         if constexpr (T::kBytes == 4) {
-            asm volatile("st.global.u32 [%0], %1;" :: "l"(p), "r"(w[i]) : "memory");
+            asm volatile("{.reg .pred q; setp.ne.u32 q, %2, 0; @q st.global.u32 [%0], %1;}"
+                         :: "l"(p), "r"(w[i]), "r"(on) : "memory");
         } else {
             const unsigned short h =
                 static_cast<unsigned short>((i & 1) ? (w[i >> 1] >> 16) : (w[i >> 1] & 0xFFFFu));
-            asm volatile("st.global.u16 [%0], %1;" :: "l"(p), "h"(h) : "memory");
+            asm volatile("{.reg .pred q; setp.ne.u32 q, %2, 0; @q st.global.u16 [%0], %1;}"
+                         :: "l"(p), "h"(h), "r"(on) : "memory");
         }
     }
 };
@@ -254,6 +281,19 @@ __device__ __forceinline__ void st_slot(void *p, const Slot<F32> &s) {
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
                  :: "l"(p), "r"(s.w[0]), "r"(s.w[1]), "r"(s.w[2]), "r"(s.w[3]), "r"(s.w[4]),
                     "r"(s.w[5]), "r"(s.w[6]), "r"(s.w[7]) : "memory");
+}
+
+// The same when `on` (predicated, no branch).
+__device__ __forceinline__ void st_slot_if(bool on, void *p, const Slot<BF16> &s) {
+    asm volatile("{.reg .pred q; setp.ne.u32 q, %5, 0; @q st.global.v4.b32 [%0], {%1,%2,%3,%4};}"
+                 :: "l"(p), "r"(s.w[0]), "r"(s.w[1]), "r"(s.w[2]), "r"(s.w[3]),
+                    "r"(static_cast<uint32_t>(on)) : "memory");
+}
+__device__ __forceinline__ void st_slot_if(bool on, void *p, const Slot<F32> &s) {
+    asm volatile("{.reg .pred q; setp.ne.u32 q, %9, 0;"
+                 " @q st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};}"
+                 :: "l"(p), "r"(s.w[0]), "r"(s.w[1]), "r"(s.w[2]), "r"(s.w[3]), "r"(s.w[4]),
+                    "r"(s.w[5]), "r"(s.w[6]), "r"(s.w[7]), "r"(static_cast<uint32_t>(on)) : "memory");
 }
 
 // One element of T at p.

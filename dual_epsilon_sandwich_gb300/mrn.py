@@ -504,62 +504,84 @@ def seam_scale(u, gamma, out=None):
 # ---------------------------------------------------------------------------
 # Training: LayerNorm, dropout before the residual add, and the gradients.  All
 # tensors of a call are on one device, which need not be the current one; the
-# work runs on that device's current stream.
+# work runs on that device's current stream.  (The checks take one test per tensor
+# where nothing is wrong: a call's host time is what a small call costs.)
 # ---------------------------------------------------------------------------
 def _train_rows(x, name):
-    """(rows, n, dtype code) of the tensor that fixes a call's shape, type and device."""
+    """(rows, n, dtype code, device index) of the tensor that fixes a call's shape."""
     dt = _dtype_code(x)
-    _check(x, name, x.dtype)
-    if x.dim() == 0:
+    dev = x.get_device()
+    if dev < 0 or not x.is_contiguous():
+        _check(x, name, x.dtype)
+    shape = x.shape
+    if not shape:
         raise ValueError(f"{name} must have at least one dimension")
-    rows, n = _rows_n(x)
-    return rows, n, dt
+    n = shape[-1]
+    return (x.numel() // n if n else 0), n, dt, dev
 
 
-def _train_check(t, name, like, dtype, shape):
-    _check(t, name, dtype, shape)
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+def _fits(t, name, dtype, shape, dev):
+    """t is a contiguous tensor of this type and shape on device dev, or it is refused."""
+    if t.dtype != dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        _check(t, name, dtype, shape)
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
 
 
-def _ptr(t):
-    return 0 if t is None else t.data_ptr()
-
-
-def _rng_ptr(rng, like, p):
+def _rng_ptr(rng, dev, p):
     """rng: int64 or uint64 tensor {seed, offset} on the device; None when p == 0."""
     import torch
     if rng is None:
         if p != 0:
             raise ValueError("rng is required when p > 0")
         return 0
-    if rng.dtype not in (torch.int64, torch.uint64):
+    if rng.dtype != torch.int64 and rng.dtype != torch.uint64:
         raise TypeError(f"rng has dtype {rng.dtype}, expected int64 or uint64")
-    _train_check(rng, "rng", like, rng.dtype, (2,))
+    _fits(rng, "rng", rng.dtype, (2,), dev)
     return rng.data_ptr()
 
 
-def _run(what, like, fn, *args):
-    """fn(*args, stream) on like's device and that device's current stream."""
+def _run(what, dev, fn, *args):
+    """fn(*args, stream) on device dev and its current stream."""
     import torch
-    if like.device.index == torch.cuda.current_device():
-        st = fn(*args, _stream(like))
+    if dev == torch._C._cuda_getDevice():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
-        with torch.cuda.device(like.device):
-            st = fn(*args, _stream(like))
+        with torch.cuda.device(dev):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     if st != 0:
         raise MrnError(st, what)
 
 
-def _stats(mean, rstd, like, rows):
+def _stats(mean, rstd, rows, dev):
+    """Pointers of the row statistics; both or neither."""
     import torch
-    if (mean is None) != (rstd is None):
+    if mean is None and rstd is None:
+        return 0, 0
+    if mean is None or rstd is None:
         raise ValueError("mean and rstd are given together or not at all")
-    if mean is not None:
-        for t, name in ((mean, "mean"), (rstd, "rstd")):
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        if t.dtype != torch.float32 or t.get_device() != dev or t.numel() != rows or \
+                not t.is_contiguous():
             _check(t, name, torch.float32)
-            if t.device != like.device or t.numel() != rows:
-                raise ValueError(f"{name} must hold one value per row ({rows}) on {like.device}")
+            raise ValueError(f"{name} must hold one value per row ({rows}) on cuda:{dev}")
+    return mean.data_ptr(), rstd.data_ptr()
+
+
+def _row_output(t, name, x, dev):
+    """t, or a new tensor like x when it is None."""
+    if t is None:
+        import torch
+        return torch.empty_like(x)
+    _fits(t, name, x.dtype, x.shape, dev)
+    return t
+
+
+def _weight_gradient(t, name, n, x, dev):
+    import torch
+    if t is None:
+        return torch.empty(n, dtype=torch.float32, device=x.device)
+    _fits(t, name, torch.float32, (n,), dev)
+    return t
 
 
 def norm_backward_workspace(x):
@@ -567,19 +589,20 @@ def norm_backward_workspace(x):
     on x's device.  Reusable by later calls of this shape on one stream; calls that
     may run at the same time need one each."""
     import torch
-    rows, n, _ = _train_rows(x, "x")
-    with torch.cuda.device(x.device):
+    rows, n, _, dev = _train_rows(x, "x")
+    with torch.cuda.device(dev):
         return torch.empty(mrn_norm_backward_workspace(rows, n), dtype=torch.uint8,
                            device=x.device)
 
 
-def _workspace(workspace, x):
+def _workspace(workspace, x, dev):
     import torch
     if workspace is None:
         return norm_backward_workspace(x)
-    _check(workspace, "workspace", torch.uint8)
-    if workspace.device != x.device:
-        raise ValueError(f"workspace is on {workspace.device}, expected {x.device}")
+    if workspace.dtype != torch.uint8 or workspace.get_device() != dev or \
+            not workspace.is_contiguous():
+        _check(workspace, "workspace", torch.uint8)
+        raise ValueError(f"workspace is on {workspace.device}, expected cuda:{dev}")
     return workspace
 
 
@@ -587,30 +610,27 @@ def layernorm(x, gamma, beta, eps: float, out=None, mean=None, rstd=None):
     """LayerNorm over the last dimension; beta may be None, out may be x.  mean and
     rstd (float32, one per row), when given, receive the row statistics that
     layernorm_backward takes."""
-    import torch
-    rows, n, dt = _train_rows(x, "x")
-    _train_check(gamma, "gamma", x, x.dtype, (n,))
+    rows, n, dt, dev = _train_rows(x, "x")
+    _fits(gamma, "gamma", x.dtype, (n,), dev)
     if beta is not None:
-        _train_check(beta, "beta", x, x.dtype, (n,))
-    _stats(mean, rstd, x, rows)
-    out = torch.empty_like(x) if out is None else out
-    _train_check(out, "out", x, x.dtype, x.shape)
-    _run("mrn_layernorm", x, mrn_layernorm, x.data_ptr(), gamma.data_ptr(), _ptr(beta),
-         out.data_ptr(), _ptr(mean), _ptr(rstd), rows, n, eps, dt)
+        _fits(beta, "beta", x.dtype, (n,), dev)
+    pm, pr = _stats(mean, rstd, rows, dev)
+    out = _row_output(out, "out", x, dev)
+    _run("mrn_layernorm", dev, lib().mrn_layernorm, x.data_ptr(), gamma.data_ptr(),
+         0 if beta is None else beta.data_ptr(), out.data_ptr(), pm, pr, rows, n, eps, dt)
     return out
 
 
 def dropout_add(x, residual, p: float, rng, site: int = 0, out=None):
     """residual + dropout(x); residual None gives dropout(x) alone, which is also the
     gradient's form.  rng: device tensor {seed, offset}; out may be x or residual."""
-    import torch
-    rows, n, dt = _train_rows(x, "x")
+    rows, n, dt, dev = _train_rows(x, "x")
     if residual is not None:
-        _train_check(residual, "residual", x, x.dtype, x.shape)
-    out = torch.empty_like(x) if out is None else out
-    _train_check(out, "out", x, x.dtype, x.shape)
-    _run("mrn_dropout_add", x, mrn_dropout_add, x.data_ptr(), _ptr(residual), out.data_ptr(),
-         _rng_ptr(rng, x, p), site, p, rows, n, dt)
+        _fits(residual, "residual", x.dtype, x.shape, dev)
+    out = _row_output(out, "out", x, dev)
+    _run("mrn_dropout_add", dev, lib().mrn_dropout_add, x.data_ptr(),
+         0 if residual is None else residual.data_ptr(), out.data_ptr(), _rng_ptr(rng, dev, p),
+         site, p, rows, n, dt)
     return out
 
 
@@ -618,52 +638,37 @@ def dropout_add_layernorm(x, residual, gamma, beta, eps: float, p: float, rng, s
                           out_stream=None, normed=None, mean=None, rstd=None):
     """(out_stream, normed): out_stream = residual + dropout(x), normed =
     layernorm(out_stream).  out_stream may be x or residual (in place)."""
-    import torch
-    rows, n, dt = _train_rows(x, "x")
-    _train_check(residual, "residual", x, x.dtype, x.shape)
-    _train_check(gamma, "gamma", x, x.dtype, (n,))
+    rows, n, dt, dev = _train_rows(x, "x")
+    _fits(residual, "residual", x.dtype, x.shape, dev)
+    _fits(gamma, "gamma", x.dtype, (n,), dev)
     if beta is not None:
-        _train_check(beta, "beta", x, x.dtype, (n,))
-    _stats(mean, rstd, x, rows)
-    out_stream = torch.empty_like(x) if out_stream is None else out_stream
-    normed = torch.empty_like(x) if normed is None else normed
-    _train_check(out_stream, "out_stream", x, x.dtype, x.shape)
-    _train_check(normed, "normed", x, x.dtype, x.shape)
-    _run("mrn_dropout_add_layernorm", x, mrn_dropout_add_layernorm, x.data_ptr(),
-         residual.data_ptr(), gamma.data_ptr(), _ptr(beta), out_stream.data_ptr(),
-         normed.data_ptr(), _ptr(mean), _ptr(rstd), _rng_ptr(rng, x, p), site, p, rows, n, eps, dt)
+        _fits(beta, "beta", x.dtype, (n,), dev)
+    pm, pr = _stats(mean, rstd, rows, dev)
+    out_stream = _row_output(out_stream, "out_stream", x, dev)
+    normed = _row_output(normed, "normed", x, dev)
+    _run("mrn_dropout_add_layernorm", dev, lib().mrn_dropout_add_layernorm, x.data_ptr(),
+         residual.data_ptr(), gamma.data_ptr(), 0 if beta is None else beta.data_ptr(),
+         out_stream.data_ptr(), normed.data_ptr(), pm, pr, _rng_ptr(rng, dev, p), site, p, rows,
+         n, eps, dt)
     return out_stream, normed
 
 
 def _backward_operands(dy, x, gamma, dstream, dx, dgamma):
-    import torch
-    rows, n, dt = _train_rows(x, "x")
-    _train_check(dy, "dy", x, x.dtype, x.shape)
-    _train_check(gamma, "gamma", x, x.dtype, (n,))
+    rows, n, dt, dev = _train_rows(x, "x")
+    _fits(dy, "dy", x.dtype, x.shape, dev)
+    _fits(gamma, "gamma", x.dtype, (n,), dev)
+    pd = 0
     if dstream is not None:
-        _train_check(dstream, "dstream", x, x.dtype, x.shape)
-    dx = torch.empty_like(x) if dx is None else dx
-    _train_check(dx, "dx", x, x.dtype, x.shape)
-    if dgamma is None:
-        dgamma = torch.empty(n, dtype=torch.float32, device=x.device)
-    _train_check(dgamma, "dgamma", x, torch.float32, (n,))
-    return rows, n, dt, dx, dgamma
+        _fits(dstream, "dstream", x.dtype, x.shape, dev)
+        pd = dstream.data_ptr()
+    return rows, n, dt, dev, pd, _row_output(dx, "dx", x, dev), \
+        _weight_gradient(dgamma, "dgamma", n, x, dev)
 
 
-def _dbeta(dbeta, bias, x, n):
-    import torch
-    if not bias:
-        return None
-    if dbeta is None:
-        dbeta = torch.empty(n, dtype=torch.float32, device=x.device)
-    _train_check(dbeta, "dbeta", x, torch.float32, (n,))
-    return dbeta
-
-
-def _need_stats(mean, rstd, x, rows):
+def _need_stats(mean, rstd, rows, dev):
     if mean is None or rstd is None:
         raise ValueError("mean and rstd of the forward pass are required")
-    _stats(mean, rstd, x, rows)
+    return _stats(mean, rstd, rows, dev)
 
 
 def layernorm_backward(dy, x, gamma, mean, rstd, dstream=None, dx=None, dgamma=None, dbeta=None,
@@ -671,13 +676,13 @@ def layernorm_backward(dy, x, gamma, mean, rstd, dstream=None, dx=None, dgamma=N
     """(dx, dgamma, dbeta) of layernorm; dgamma and dbeta are float32, dbeta is None
     when bias is false.  dstream, when given, is added to dx; dx may be dy, x or
     dstream.  workspace: norm_backward_workspace(x), allocated here when None."""
-    rows, n, dt, dx, dgamma = _backward_operands(dy, x, gamma, dstream, dx, dgamma)
-    _need_stats(mean, rstd, x, rows)
-    dbeta = _dbeta(dbeta, bias, x, n)
-    ws = _workspace(workspace, x)
-    _run("mrn_layernorm_backward", x, mrn_layernorm_backward, dy.data_ptr(), x.data_ptr(),
-         gamma.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ptr(dstream), dx.data_ptr(),
-         dgamma.data_ptr(), _ptr(dbeta), ws.data_ptr(), ws.numel(), rows, n, dt)
+    rows, n, dt, dev, pd, dx, dgamma = _backward_operands(dy, x, gamma, dstream, dx, dgamma)
+    pm, pr = _need_stats(mean, rstd, rows, dev)
+    dbeta = _weight_gradient(dbeta, "dbeta", n, x, dev) if bias else None
+    ws = _workspace(workspace, x, dev)
+    _run("mrn_layernorm_backward", dev, lib().mrn_layernorm_backward, dy.data_ptr(),
+         x.data_ptr(), gamma.data_ptr(), pm, pr, pd, dx.data_ptr(), dgamma.data_ptr(),
+         0 if dbeta is None else dbeta.data_ptr(), ws.data_ptr(), ws.numel(), rows, n, dt)
     return dx, dgamma, dbeta
 
 
@@ -686,17 +691,16 @@ def dropout_add_layernorm_backward(dnormed, out_stream, gamma, mean, rstd, p: fl
                                    dgamma=None, dbeta=None, bias: bool = True, workspace=None):
     """(dx, dresidual, dgamma, dbeta) of dropout_add_layernorm, from its out_stream,
     mean, rstd and the same p, rng values and site."""
-    import torch
-    rows, n, dt, dx, dgamma = _backward_operands(dnormed, out_stream, gamma, dstream, dx, dgamma)
-    _need_stats(mean, rstd, out_stream, rows)
-    dresidual = torch.empty_like(out_stream) if dresidual is None else dresidual
-    _train_check(dresidual, "dresidual", out_stream, out_stream.dtype, out_stream.shape)
-    dbeta = _dbeta(dbeta, bias, out_stream, n)
-    ws = _workspace(workspace, out_stream)
-    _run("mrn_dropout_add_layernorm_backward", out_stream, mrn_dropout_add_layernorm_backward,
-         dnormed.data_ptr(), out_stream.data_ptr(), gamma.data_ptr(), mean.data_ptr(),
-         rstd.data_ptr(), _ptr(dstream), dx.data_ptr(), dresidual.data_ptr(), dgamma.data_ptr(),
-         _ptr(dbeta), _rng_ptr(rng, out_stream, p), site, p, ws.data_ptr(), ws.numel(), rows, n, dt)
+    rows, n, dt, dev, pd, dx, dgamma = _backward_operands(dnormed, out_stream, gamma, dstream, dx,
+                                                          dgamma)
+    pm, pr = _need_stats(mean, rstd, rows, dev)
+    dresidual = _row_output(dresidual, "dresidual", out_stream, dev)
+    dbeta = _weight_gradient(dbeta, "dbeta", n, out_stream, dev) if bias else None
+    ws = _workspace(workspace, out_stream, dev)
+    _run("mrn_dropout_add_layernorm_backward", dev, lib().mrn_dropout_add_layernorm_backward,
+         dnormed.data_ptr(), out_stream.data_ptr(), gamma.data_ptr(), pm, pr, pd, dx.data_ptr(),
+         dresidual.data_ptr(), dgamma.data_ptr(), 0 if dbeta is None else dbeta.data_ptr(),
+         _rng_ptr(rng, dev, p), site, p, ws.data_ptr(), ws.numel(), rows, n, dt)
     return dx, dresidual, dgamma, dbeta
 
 
@@ -704,9 +708,9 @@ def rmsnorm_backward(dy, x, gamma, eps: float, dstream=None, dx=None, dgamma=Non
                      workspace=None):
     """(dx, dgamma) of rmsnorm; dgamma is float32.  dstream, when given, is added to
     dx; dx may be dy, x or dstream."""
-    rows, n, dt, dx, dgamma = _backward_operands(dy, x, gamma, dstream, dx, dgamma)
-    ws = _workspace(workspace, x)
-    _run("mrn_rmsnorm_backward", x, mrn_rmsnorm_backward, dy.data_ptr(), x.data_ptr(),
-         gamma.data_ptr(), _ptr(dstream), dx.data_ptr(), dgamma.data_ptr(), ws.data_ptr(),
-         ws.numel(), rows, n, eps, dt)
+    rows, n, dt, dev, pd, dx, dgamma = _backward_operands(dy, x, gamma, dstream, dx, dgamma)
+    ws = _workspace(workspace, x, dev)
+    _run("mrn_rmsnorm_backward", dev, lib().mrn_rmsnorm_backward, dy.data_ptr(), x.data_ptr(),
+         gamma.data_ptr(), pd, dx.data_ptr(), dgamma.data_ptr(), ws.data_ptr(), ws.numel(), rows,
+         n, eps, dt)
     return dx, dgamma
