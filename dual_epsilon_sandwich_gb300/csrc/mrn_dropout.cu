@@ -32,12 +32,16 @@ __global__ void __launch_bounds__(kDropoutThreads) mrn_dropout_kernel(const Drop
                 if (ADD) ld_slot(r[k], elem_ptr<T>(a.res, e));
             }
         }
+        DropGroup drop[kDropoutGroups];
+        uint64_t group[kDropoutGroups];
+#pragma unroll
+        for (int k = 0; k < kDropoutGroups; ++k) group[k] = static_cast<uint64_t>(g0 + k * kDropoutThreads);
+        drop_groups<kDropoutGroups>(drop, key, group, a.drop.threshold);
 #pragma unroll
         for (int k = 0; k < kDropoutGroups; ++k) {
-            const int64_t g = g0 + k * kDropoutThreads;
-            const int64_t e = g * 8;
+            const int64_t e = (g0 + k * kDropoutThreads) * 8;
             if (e >= a.total) continue;
-            const DropGroup d = drop_group(key, static_cast<uint64_t>(g), a.drop.threshold);
+            const DropGroup &d = drop[k];
             if (VEC && e + 8 <= a.total) {
                 float o[8];
 #pragma unroll

@@ -109,19 +109,21 @@ mrn_layernorm_tile_kernel(const LayernormArgs a, const TileArgs t) {
         const uint32_t from = ring + walk.read * walk.bytes;
         Slot<T> v[R][K];
         float sum[R], end[R];
+        bool end_keep[R];
 #pragma unroll
         for (int rr = 0; rr < R; ++rr) {
             tile.fetch(v[rr], from, 0, rr, kOps);
             if constexpr (ADD) {
                 Slot<T> res[K];
+                DropGroup d[K];
+                end_keep[rr] = tile.masks(d, key, rr, a.drop.threshold);
                 tile.fetch(res, from, 1, rr, kOps);
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
-                    const DropGroup d = drop_group(key, tile.group(rr, k), a.drop.threshold);
                     float o[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        o[i] = drop_add(v[rr][k].get(i), res[k].get(i), d.keeps(i), a.drop.scale);
+                        o[i] = drop_add(v[rr][k].get(i), res[k].get(i), d[k].keeps(i), a.drop.scale);
                     v[rr][k].put(o);
                 }
                 tile.store(stream_out, rr, tile.valid(rr), v[rr]);
@@ -137,10 +139,9 @@ mrn_layernorm_tile_kernel(const LayernormArgs a, const TileArgs t) {
             if (EDGE && tile.ends) {
                 end[rr] = tile.fetch_end(end_w, walk.read, 0, rr);
                 if constexpr (ADD) {
-                    const bool keep = drop_keeps_element(key, tile.end_element(rr), a.drop.threshold);
                     end[rr] = tile.store_end(stream_out, rr, tile.valid(rr),
                                              drop_add(end[rr], tile.fetch_end(end_w, walk.read, 1, rr),
-                                                      keep, a.drop.scale));
+                                                      end_keep[rr], a.drop.scale));
                     if (tile.end_col < 0) end[rr] = 0.0f;
                 }
                 sum[rr] += end[rr];

@@ -179,7 +179,7 @@ mrn_norm_backward_tile_kernel(const BackwardArgs a, const TileArgs t, float *par
             }
         }
         float s[2] = {f2_sum(s0), f2_sum(s1)};
-        float end_d = 0.0f, end_xh = 0.0f;
+        float end_d = 0.0f, end_xh = 0.0f, end_o = 0.0f;
         if (EDGE && tile.ends) {
             end_d = tile.fetch_end(end_w, walk.read, 0, 0);
             end_xh = tile.fetch_end(end_w, walk.read, 1, 0);
@@ -237,24 +237,22 @@ mrn_norm_backward_tile_kernel(const BackwardArgs a, const TileArgs t, float *par
             float o = fmaf(end_xh, c2, RMS ? ew * rstd : fmaf(ew, rstd, c1));
             if (RMS) end_sum_g = fmaf(end_d, end_xh * rstd, end_sum_g);
             if (a.dstream) o += tile.fetch_end(end_w, walk.read, 2, 0);
-            if (a.dres) {
-                tile.store_end(dres, 0, ok, o);
-                const bool keep = drop_keeps_element(key, tile.end_element(0), a.drop.threshold);
-                o = drop_scale(o, keep, a.drop.scale);
-            }
-            tile.store_end(dx, 0, ok, o);
+            end_o = o;
+            tile.store_end(a.dres ? dres : dx, 0, ok, o);
         }
         if (a.dres) {
+            DropGroup g[K];
+            const bool end_keep = tile.masks(g, key, 0, a.drop.threshold);
             tile.store(dres, 0, ok, out);
+            if (EDGE && tile.ends) tile.store_end(dx, 0, ok, drop_scale(end_o, end_keep, a.drop.scale));
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const DropGroup g = drop_group(key, tile.group(0, k), a.drop.threshold);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     float lo, hi;
                     f2_unpack(w[k][i], lo, hi);
-                    out[k].put_pair(i, f2_pack(drop_scale(lo, g.keeps(2 * i), a.drop.scale),
-                                               drop_scale(hi, g.keeps(2 * i + 1), a.drop.scale)));
+                    out[k].put_pair(i, f2_pack(drop_scale(lo, g[k].keeps(2 * i), a.drop.scale),
+                                               drop_scale(hi, g[k].keeps(2 * i + 1), a.drop.scale)));
                 }
             }
         }

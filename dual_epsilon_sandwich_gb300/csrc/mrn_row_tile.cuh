@@ -332,6 +332,27 @@ template <class T, int K, int R, bool EDGE, bool WARP> struct RowTile {
     __device__ __forceinline__ int64_t end_element(int rr) const {
         return (at + rr * step) / T::kBytes + end_col - before;
     }
+    // The masks of row rr's slots, and whether the single element is kept: its group is
+    // evaluated beside theirs in the one warp that needs it.
+    __device__ __forceinline__ bool masks(DropGroup (&d)[K], const DropKey &key, int rr, uint32_t threshold) const {
+        if (EDGE && ends) {
+            DropGroup e[K + 1];
+            uint64_t g[K + 1];
+#pragma unroll
+            for (int k = 0; k < K; ++k) g[k] = group(rr, k);
+            const int64_t element = end_element(rr);
+            g[K] = static_cast<uint64_t>(element) >> 3;
+            drop_groups<K + 1>(e, key, g, threshold);
+#pragma unroll
+            for (int k = 0; k < K; ++k) d[k] = e[k];
+            return e[K].keeps_any(static_cast<int>(element & 7));
+        }
+        uint64_t g[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k) g[k] = group(rr, k);
+        drop_groups<K>(d, key, g, threshold);
+        return false;
+    }
     // The thread's columns of a weight vector, zeros outside the row; once per CTA.  All
     // loads are independent of each other.
     __device__ __forceinline__ void weights(Slot<T> (&s)[K], const void *w) const {

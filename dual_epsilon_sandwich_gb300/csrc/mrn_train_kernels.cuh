@@ -35,58 +35,80 @@ __device__ __forceinline__ DropKey drop_key(const DropArgs &d) {
     return k;
 }
 
-// The eight 16-bit lanes of group e / 8, two per word, low half first.
-__device__ __forceinline__ void philox_lanes(const DropKey &key, uint64_t group, uint32_t (&w)[4]) {
-    uint32_t c0 = static_cast<uint32_t>(group), c1 = static_cast<uint32_t>(group >> 32);
-    uint32_t c2 = key.c2, c3 = key.c3, k0 = key.k0, k1 = key.k1;
-#pragma unroll
-    for (int r = 0; r < 10; ++r) {
-        const uint64_t a = static_cast<uint64_t>(c0) * 0xD2511F53u;
-        const uint64_t b = static_cast<uint64_t>(c2) * 0xCD9E8D57u;
-        c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ k0;
-        c1 = static_cast<uint32_t>(b);
-        c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ k1;
-        c3 = static_cast<uint32_t>(a);
-        k0 += 0x9E3779B9u;
-        k1 += 0xBB67AE85u;
-    }
-    w[0] = c0;
-    w[1] = c1;
-    w[2] = c2;
-    w[3] = c3;
-}
-
-// One group's lanes and the word threshold they are compared with: element i is kept when
-// its lane, moved to the upper half of a word, is >= at (the lower half left below an upper
-// lane does not change the comparison).  All kept (threshold 0) and all dropped (65536) need
-// no generator.
+// One group's eight 16-bit lanes (two per word, low half first) and the word threshold they
+// are compared with: element i is kept when its lane, moved to the upper half of a word, is
+// >= at (the lower half left below an upper lane does not change the comparison).
 struct DropGroup {
     uint32_t w[4];
     uint32_t at;
     __device__ __forceinline__ bool keeps(int i) const {
         return ((i & 1) ? w[i >> 1] : w[i >> 1] << 16) >= at;
     }
+    // the same for a lane that is not known when compiling
+    __device__ __forceinline__ bool keeps_any(int i) const {
+        const uint32_t word = i < 4 ? (i < 2 ? w[0] : w[1]) : (i < 6 ? w[2] : w[3]);
+        return ((i & 1) ? word : word << 16) >= at;
+    }
 };
+
+// G groups, round by round: the round keys are advanced once for all of them, and the G
+// chains of ten dependent multiplications overlap.  All kept (threshold 0) and all dropped
+// (65536) need no generator.
+template <int G>
+__device__ __forceinline__ void drop_groups(DropGroup (&d)[G], const DropKey &key, const uint64_t (&group)[G],
+                                            uint32_t threshold) {
+    const bool mixed = threshold != 0u && threshold < 65536u;
+    uint32_t c0[G], c1[G], c2[G], c3[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        d[g].at = mixed ? threshold << 16 : (threshold == 0u ? 0u : 1u);
+        c0[g] = c1[g] = c2[g] = c3[g] = 0u;
+    }
+    if (mixed) {
+        uint32_t k0 = key.k0, k1 = key.k1;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            c0[g] = static_cast<uint32_t>(group[g]);
+            c1[g] = static_cast<uint32_t>(group[g] >> 32);
+            c2[g] = key.c2;
+            c3[g] = key.c3;
+        }
+#pragma unroll
+        for (int r = 0; r < 10; ++r) {
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const uint64_t a = static_cast<uint64_t>(c0[g]) * 0xD2511F53u;
+                const uint64_t b = static_cast<uint64_t>(c2[g]) * 0xCD9E8D57u;
+                c0[g] = static_cast<uint32_t>(b >> 32) ^ c1[g] ^ k0;
+                c1[g] = static_cast<uint32_t>(b);
+                c2[g] = static_cast<uint32_t>(a >> 32) ^ c3[g] ^ k1;
+                c3[g] = static_cast<uint32_t>(a);
+            }
+            k0 += 0x9E3779B9u;
+            k1 += 0xBB67AE85u;
+        }
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        d[g].w[0] = c0[g];
+        d[g].w[1] = c1[g];
+        d[g].w[2] = c2[g];
+        d[g].w[3] = c3[g];
+    }
+}
 
 __device__ __forceinline__ DropGroup drop_group(const DropKey &key, uint64_t group,
                                                 uint32_t threshold) {
-    DropGroup g;
-    g.w[0] = g.w[1] = g.w[2] = g.w[3] = 0u;
-    g.at = threshold == 0u ? 0u : 1u;
-    if (threshold != 0u && threshold < 65536u) {
-        philox_lanes(key, group, g.w);
-        g.at = threshold << 16;
-    }
-    return g;
+    DropGroup d[1];
+    const uint64_t g[1] = {group};
+    drop_groups<1>(d, key, g, threshold);
+    return d[0];
 }
 
 // One element on its own.
 __device__ __forceinline__ bool drop_keeps_element(const DropKey &key, int64_t e,
                                                    uint32_t threshold) {
-    const DropGroup g = drop_group(key, static_cast<uint64_t>(e) >> 3, threshold);
-    const int i = static_cast<int>(e & 7);
-    const uint32_t word = i < 4 ? (i < 2 ? g.w[0] : g.w[1]) : (i < 6 ? g.w[2] : g.w[3]);
-    return ((i & 1) ? word : word << 16) >= g.at;
+    return drop_group(key, static_cast<uint64_t>(e) >> 3, threshold).keeps_any(static_cast<int>(e & 7));
 }
 
 // 1 / sqrt(v): within 2 units in the last place (rsqrtf), and 0 at infinity.  The IEEE
