@@ -73,7 +73,6 @@ mrn_layernorm_tile_kernel(const LayernormArgs a, const TileArgs t) {
     __shared__ RowSumSlots<R> slots;
     constexpr int kOps = ADD ? 2 : 1;
     __shared__ EndSlots<kOps, R, EDGE, WARP> end_w;
-    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(ring_bytes));
     RowTile<T, K, R, EDGE, WARP> tile(a.rows, a.n, t);
     const int64_t back = static_cast<int64_t>(t.mis) * T::kBytes;
     const char *ops[kOps];
@@ -81,12 +80,13 @@ mrn_layernorm_tile_kernel(const LayernormArgs a, const TileArgs t) {
     if constexpr (ADD) ops[1] = static_cast<const char *>(a.res) - back;
     char *const y = static_cast<char *>(a.y) - back;
     char *const stream_out = ADD ? static_cast<char *>(a.stream_out) - back : nullptr;
-    RingWalk walk(R * kOps * K * tile.region, t.stages);
+    RingWalk walk(tile.stage_bytes(kOps), t.stages);
     const int ahead = t.stages - 1;
+    const uint32_t ring = tile.warp_ring(static_cast<uint32_t>(__cvta_generic_to_shared(ring_bytes)), t.stages, kOps);
     tile.clear(ring, t.stages, kOps);
     row_sum_setup(slots, tile.cl);
     pdl_enter();
-    for (int s = 0; s < ahead; ++s) tile.issue(ring + s * walk.bytes, s, s, ops, kOps, end_w);
+    for (int s = 0; s < ahead; ++s) tile.issue(ring + s * walk.bytes, s, ops, kOps, end_w);
     const DropKey key = ADD ? drop_key(a.drop) : DropKey{};
     Slot<T> gamma[K], beta[K];
     tile.weights(gamma, a.gamma);
@@ -103,7 +103,7 @@ mrn_layernorm_tile_kernel(const LayernormArgs a, const TileArgs t) {
     int turn = 0;
     for (; tile.cta_left > 0; tile.advance(), walk.next()) {
         __syncwarp();
-        tile.issue(ring + walk.write * walk.bytes, walk.write, ahead, ops, kOps, end_w);
+        tile.issue(ring + walk.write * walk.bytes, walk.write, ops, kOps, end_w);
         cp_async_wait(ahead);
         __syncwarp();
         const uint32_t from = ring + walk.read * walk.bytes;
@@ -226,24 +226,37 @@ bool launch_layernorm_k(const LayernormArgs &a, const TileShape &p, int sms, boo
                   : launch_layernorm_tile<T, K, R, false, WARP, false>(a, p, sms, pdl, stream, launches, err);
 }
 
-// Slots per thread and rows at a time for rows of a CTA.  Measured on GB300, a 200 to 250 MB
-// call each, against the next best of k = 1..4, r = 1..2 (us):
-//   bf16, alone:      n = 2048 2 x 2 32.7 (4 x 1 33.3), 4096 4 x 1 33.4 (2 x 2 35.5), 8192 4 x 1
-//                     32.3 (2 x 2 37.4), 16384 4 x 1 54.6 (4 x 2 57.5)
-//   bf16, after add:  n = 4096 2 x 2 64.6 (2 x 1 65.5), 5120 4 x 1 65.8 (2 x 2 66.2), 8192 4 x 1
-//                     63.8 (2 x 2 65.3)
-//   f32, alone:       n = 4096 1 x 1 32.2 (3 x 1 32.8), 8192 2 x 2 32.8 (4 x 2 32.9), 12288 4 x 1
-//                     50.3 (3 x 1 58.4)
-//   f32, after add:   n = 4096 1 x 1 63.0 (3 x 2 64.9), 6656 4 x 1 63.8 (3 x 1 65.3)
-template <class T> void forward_tile(int64_t slots, bool add, int *k, int *r) {
-    if (T::kBytes == 2) {
-        const bool narrow = slots <= (add ? 576 : 320);
-        *k = narrow ? 2 : 4;
-        *r = narrow ? 2 : 1;
+// Slots per thread (k) and rows at a time (r) for rows of a CTA.  Measured on GB300, a call of
+// 220 MB (alone) or 440 MB (after the add), k x r (us):
+//   bf16 alone      n = 1536 2 x 2 45.9, 4 x 1 48.1;  2048 4 x 1 45.2, 2 x 2 45.3;  4096 4 x 1
+//                   44.4, 2 x 2 47.2;  4095 4 x 1 50.2, 2 x 2 61;  8192 4 x 1 43, 2 x 2 50
+//   bf16 after add  n = 2048 4 x 1 94.4;  4096 2 x 2 89.9, 4 x 1 93;  4095 4 x 1 90.5, 2 x 2
+//                   111;  5120 4 x 1 88, 2 x 2 89;  8192 4 x 1 86, 2 x 2 88
+//   f32 alone       n = 4096 1 x 1 43, 4 x 1 45;  6656 2 x 2 38.9, 4 x 1 40;  6655 2 x 2 42.1, 4
+//                   x 1 46.2;  12288 4 x 1 50, 2 x 1 58
+//   f32 after add   n = 4096 1 x 1 63, 4 x 2 65;  5120 2 x 1 72.3, 4 x 1 76.2;  6655 2 x 1 75.9,
+//                   4 x 1 79;  6656 4 x 1 72.0, 2 x 1 73;  8191 4 x 1 77.7, 2 x 1 79
+// Rows in clusters, and their CTAs' threads (us): f32 alone 4096 x 16384 2 x 2 of 128 98.8, 2 x 1
+// of 512 104.7, 4 x 1 of 384 132; 2048 x 32768 2 x 1 of 256 107, 2 x 2 of 128 115.  f32 after add
+// 4096 x 16384 2 x 1 of 256 176, 4 x 1 198.  bf16 alone 2048 x 32768 4 x 1 of 128 66, of 512 72.
+template <class T> void forward_tile(int64_t slots, bool add, bool edge, int *k, int *r, int *threads) {
+    if (T::kBytes == 4 && slots > 1536) {
+        *k = 2;
+        *r = !add && slots <= 2048 ? 2 : 1;
+        *threads = *r == 2 ? 128 : 256;
+    } else if (T::kBytes == 2) {
+        const bool two = slots <= 192 || (add && !edge && slots > 320 && slots <= 576);
+        *k = two ? 2 : 4;
+        *r = two ? 2 : 1;
+    } else if (add) {
+        *k = slots <= 512 ? 1 : (slots <= 896 ? 2 : 4);
+        *r = 1;
     } else {
-        *k = slots <= 512 ? 1 : (slots <= 1024 && !add ? 2 : 4);
+        *k = slots <= 512 ? 1 : (slots <= 1024 ? 2 : 4);
         *r = *k == 2 ? 2 : 1;
     }
+    if (T::kBytes == 2 && slots > 2048) *threads = 128;
+    while (*threads > 0 && *threads < forward_threads<T>(*k, *r) && slots > int64_t(kMaxCluster) * *k * *threads) *threads *= 2;
 }
 
 template <class T>
@@ -252,12 +265,16 @@ cudaError_t launch_layernorm_typed(const LayernormArgs &a, int sms, bool pdl, cu
     const int mis = common_offset(T::kBytes, a.x, a.y, a.res, static_cast<const void *>(a.stream_out));
     // (a generator group is a slot only when the operands start on a slot boundary)
     if (mis == 0 || (mis > 0 && a.drop.threshold == 0)) {
-        int k = 4, r = 1;
-        forward_tile<T>(a.n / 8, a.res != nullptr, &k, &r);
+        int k = 4, r = 1, most_threads = 0;
+        forward_tile<T>(a.n / 8, a.res != nullptr, mis != 0 || a.n % 8 != 0, &k, &r, &most_threads);
+        if (most_threads == 0 || most_threads > forward_threads<T>(k, r)) most_threads = forward_threads<T>(k, r);
         //KR
         const bool few = tile_few_rows(a.rows, a.n, sms);
-        if (few) k = r = 1;
-        const TileShape p = tile_shape(a.n, mis, k, few ? tile_few_threads(a.rows, a.n, sms) : forward_threads<T>(k, r), few);
+        if (few) {
+            k = r = 1;
+            most_threads = tile_few_threads(a.rows, a.n, sms);
+        }
+        const TileShape p = tile_shape(a.n, mis, k, most_threads, few);
         cudaError_t err = cudaSuccess;
         bool done = false;
         if (p.ok && p.warp) {
@@ -268,6 +285,7 @@ cudaError_t launch_layernorm_typed(const LayernormArgs &a, int sms, bool pdl, cu
         } else if (p.ok) {
             //MORE
             if (k == 1) done = launch_layernorm_k<T, 1, 1, false>(a, p, sms, pdl, stream, launches, &err);
+            else if (T::kBytes == 4 && k == 2 && r == 1) done = launch_layernorm_k<T, 2, 1, false>(a, p, sms, pdl, stream, launches, &err);
             else if (k == 2) done = launch_layernorm_k<T, 2, 2, false>(a, p, sms, pdl, stream, launches, &err);
             else done = launch_layernorm_k<T, 4, 1, false>(a, p, sms, pdl, stream, launches, &err);
         }

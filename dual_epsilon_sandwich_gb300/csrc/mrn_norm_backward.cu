@@ -104,7 +104,6 @@ mrn_norm_backward_tile_kernel(const BackwardArgs a, const TileArgs t, float *par
     __shared__ RowSumSlots<2> slots;
     __shared__ float stats[kTileMaxStages][2][kWarpTileThreads];   // mean and rstd, per team
     __shared__ EndSlots<3, 1, EDGE, WARP> end_w;
-    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(ring_bytes));
     RowTile<T, K, 1, EDGE, WARP> tile(a.rows, a.n, t);
     const int ops_count = a.dstream ? 3 : 2;
     const int64_t back = static_cast<int64_t>(t.mis) * T::kBytes;
@@ -113,22 +112,27 @@ mrn_norm_backward_tile_kernel(const BackwardArgs a, const TileArgs t, float *par
         a.dstream ? static_cast<const char *>(a.dstream) - back : nullptr};
     char *const dx = static_cast<char *>(a.dx) - back;
     char *const dres = a.dres ? static_cast<char *>(a.dres) - back : nullptr;
-    RingWalk walk(ops_count * K * tile.region, t.stages);
+    RingWalk walk(tile.stage_bytes(ops_count), t.stages);
     const int ahead = t.stages - 1;
+    const uint32_t ring = tile.warp_ring(static_cast<uint32_t>(__cvta_generic_to_shared(ring_bytes)), t.stages, ops_count);
     tile.clear(ring, t.stages, ops_count);
     row_sum_setup(slots, tile.cl);
     pdl_enter();
     // mean and rstd travel with their row: a load of them in the loop held up every row
     // (16384 x 4096 bf16: 116 us against 80)
-    auto issue = [&](int to, int turns) {
-        if (!RMS && tile.leads && turns < tile.left) {
-            const int64_t r = tile.row + turns * tile.stride;
-            cp_async4(static_cast<uint32_t>(__cvta_generic_to_shared(&stats[to][0][tile.team])), a.mean + r);
-            cp_async4(static_cast<uint32_t>(__cvta_generic_to_shared(&stats[to][1][tile.team])), a.rstd + r);
+    const float *mean_of = RMS ? nullptr : a.mean + tile.row, *rstd_of = RMS ? nullptr : a.rstd + tile.row;
+    auto issue = [&](int to) {
+        if (!RMS && tile.leads) {
+            if (tile.copy_left > 0) {
+                cp_async4(static_cast<uint32_t>(__cvta_generic_to_shared(&stats[to][0][tile.team])), mean_of);
+                cp_async4(static_cast<uint32_t>(__cvta_generic_to_shared(&stats[to][1][tile.team])), rstd_of);
+            }
+            mean_of += tile.stride;
+            rstd_of += tile.stride;
         }
-        tile.issue(ring + to * walk.bytes, to, turns, ops, ops_count, end_w);
+        tile.issue(ring + to * walk.bytes, to, ops, ops_count, end_w);
     };
-    for (int s = 0; s < ahead; ++s) issue(s, s);
+    for (int s = 0; s < ahead; ++s) issue(s);
     const DropKey key = drop_key(a.drop);
     Slot<T> gamma[K];
     tile.weights(gamma, a.gamma);
@@ -144,7 +148,7 @@ mrn_norm_backward_tile_kernel(const BackwardArgs a, const TileArgs t, float *par
     row_sum_ready(tile.cl);
     for (; tile.cta_left > 0; tile.advance(), walk.next()) {
         __syncwarp();
-        issue(walk.write, ahead);
+        issue(walk.write);
         cp_async_wait(ahead);
         __syncwarp();
         const uint32_t from = ring + walk.read * walk.bytes;
@@ -278,7 +282,7 @@ mrn_norm_backward_tile_kernel(const BackwardArgs a, const TileArgs t, float *par
                     f2_unpack(which == 0 ? sum_g[k][2 * i] : sum_b[k][2 * i], f[0], f[1]);
                     f2_unpack(which == 0 ? sum_g[k][2 * i + 1] : sum_b[k][2 * i + 1], f[2], f[3]);
                     v.put(f);
-                    st_global(out + (tile.first + k * tile.width) * 8 + 4 * i, v);
+                    st_global(out + (tile.first + k * tile.slot_step()) * 8 + 4 * i, v);
                 }
             }
             if (EDGE && tile.end_col >= 0)
@@ -299,7 +303,7 @@ mrn_norm_backward_tile_kernel(const BackwardArgs a, const TileArgs t, float *par
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 if (!tile.holds(k)) continue;
-                uint64_t *to = reinterpret_cast<uint64_t *>(mine + (tile.first + k * tile.width) * 8);
+                uint64_t *to = reinterpret_cast<uint64_t *>(mine + (tile.first + k * tile.slot_step()) * 8);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) to[i] = which == 0 ? sum_g[k][i] : sum_b[k][i];
             }
@@ -464,7 +468,7 @@ cudaError_t launch_backward_typed(const BackwardArgs &a, int sms, bool pdl, cuda
         const int64_t slots = a.n / 8;
         int k = T::kBytes == 2 ? (slots <= 1024 ? 2 : 4) : (slots <= 1152 ? 3 : 2);
         int most_threads = backward_resident(k);
-        if (T::kBytes == 4 && k == 2) most_threads = 256;
+        if (T::kBytes == 4 && k == 2 && slots <= 8192) most_threads = 256;
         if (T::kBytes == 2 && k == 4) most_threads = slots <= 2048 ? 64 : (slots <= 4096 ? 128 : 256);
         //KR
         const bool few = tile_few_rows(a.rows, a.n, sms);

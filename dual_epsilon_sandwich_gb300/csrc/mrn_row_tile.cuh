@@ -2,8 +2,9 @@
 // CTA (or cluster of CTAs, or part of a warp) walks over rows that are a fixed
 // number apart, each thread owning the same columns of all of them.
 //
-//  * A thread owns K slots of eight consecutive elements, a row's width in threads
-//    apart.  Slots are cut at multiples of eight elements of the flattened matrix, so
+//  * A thread owns K slots of eight consecutive elements: a warp owns 32 K consecutive
+//    ones, a lane every 32nd of them (so that the distances between a thread's slots,
+//    in memory and in the ring, are constants of the code).  Slots are cut at multiples of eight elements of the flattened matrix, so
 //    that they are aligned in memory and are the dropout's generator groups.  When the
 //    row pitch is not a multiple of eight (EDGE), up to seven elements before the row's
 //    first whole slot and seven behind its last are taken one by one, each by a lane of
@@ -149,8 +150,11 @@ template <class T, int K, int R, bool EDGE, bool WARP> struct RowTile {
     static constexpr int kChunks = T::kBytes / 2;          // 16-byte chunks per slot
     static constexpr int kChunkElems = 8 / kChunks;
 
+    static constexpr int kBlock = 512 * kChunks;           // a warp's slots k of one operand, in bytes
+
     int width;            // threads per row (in this CTA)
-    int first;            // this thread's first slot; slot k is first + k * width
+    int lanes;            // lanes that copy together: the distance of a thread's slots
+    int first;            // this thread's first slot; slot k is first + k * lanes
     int before;           // EDGE: elements from the row's start to the next slot boundary
     unsigned cl, crank;
     int64_t row;          // this thread's first row; the R rows are `stride` apart
@@ -166,15 +170,15 @@ template <class T, int K, int R, bool EDGE, bool WARP> struct RowTile {
     int end_col;          // column of this thread's single element; -1: none
     uint32_t full;        // slots of this thread inside the row: bit k
     uint32_t copies;      // chunks this thread copies: bit k * kChunks + c
-    uint32_t region;      // bytes of one slot index k of all threads in the ring
-    uint32_t copy_base;   // this thread's place in a region: as copier,
-    uint32_t slot_base;   // ... and as owner
-    int copy_off;         // byte offset in the row of the first chunk this thread copies
-    int copy_step;        // ... and from chunk to chunk of a slot
+    uint32_t copy_to;     // this thread's place in its warp's ring: as copier,
+    uint32_t slot_from;   // ... and as owner
+    int64_t copy_at;      // the next row to copy: byte offset of this thread's first chunk
+    int copy_left;        // ... and the rows from it on
 
     __device__ __forceinline__ RowTile(int64_t rows, int64_t n, const TileArgs &t) {
         const int tid = threadIdx.x, lane = tid & 31;
-        int lanes = 32, li = lane;      // lanes that copy together, and this one's index
+        int li = lane;                  // index among the lanes that copy together
+        lanes = 32;
         team = tid >> 5;
         if constexpr (WARP) {
             cl = 1;
@@ -191,7 +195,7 @@ template <class T, int K, int R, bool EDGE, bool WARP> struct RowTile {
             cl = cluster_nctarank();
             crank = cluster_ctarank();
             width = blockDim.x;
-            first = tid + static_cast<int>(crank) * K * static_cast<int>(blockDim.x);
+            first = (static_cast<int>(crank * blockDim.x) + (tid - lane)) * K + lane;
             row = blockIdx.x / cl;
             stride = gridDim.x / cl;
         }
@@ -216,64 +220,74 @@ template <class T, int K, int R, bool EDGE, bool WARP> struct RowTile {
                 if (c < n) end_col = static_cast<int>(c);
             }
         }
-        region = blockDim.x * kChunks * 16;
         const int chunk0 = (first - li) * kChunks + li;             // chunk in the slot row
-        copy_off = chunk0 * 16;
-        copy_step = lanes * 16;
-        copy_base = static_cast<uint32_t>(((tid - li) * kChunks + li) * 16);
-        slot_base = static_cast<uint32_t>(tid * kChunks * 16);
+        copy_at = at + chunk0 * 16;
+        copy_left = left;
+        copy_to = static_cast<uint32_t>(((lane - li) * kChunks + li) * 16);
+        slot_from = static_cast<uint32_t>(lane * kChunks * 16);
         full = copies = 0u;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            if (first + k * width < slots) full |= 1u << k;
+            if (first + k * lanes < slots) full |= 1u << k;
 #pragma unroll
             for (int c = 0; c < kChunks; ++c)
-                if (chunk0 + k * width * kChunks + c * lanes < slots * kChunks)
+                if (chunk0 + (k * kChunks + c) * lanes < slots * kChunks)
                     copies |= 1u << (k * kChunks + c);
         }
     }
     __device__ __forceinline__ bool valid(int rr) const { return rr < left; }
     __device__ __forceinline__ bool holds(int k) const { return (full >> k) & 1u; }
     // First column of slot k.
-    __device__ __forceinline__ int column(int k) const { return (first + k * width) * 8 + before; }
+    __device__ __forceinline__ int slot_step() const { return WARP ? lanes : 32; }
+    __device__ __forceinline__ int column(int k) const { return (first + k * slot_step()) * 8 + before; }
+    // A warp's ring of `stages` stages of R rows of `count` operands.
+    static __device__ __forceinline__ uint32_t stage_bytes(int count) { return R * count * K * kBlock; }
+    __device__ __forceinline__ uint32_t warp_ring(uint32_t ring, int stages, int count) const {
+        return ring + (threadIdx.x >> 5) * (stages * stage_bytes(count));
+    }
 
-    // Zeroes a ring of `stages` stages of `count` operands: the chunks outside the row are
-    // never copied, and read as zeros ever after.
+    // Zeroes this warp's ring where some of its chunks lie outside the row: they are never
+    // copied, and read as zeros ever after.
     __device__ __forceinline__ void clear(uint32_t ring, int stages, int count) const {
+        if (__all_sync(0xFFFFFFFFu, copies == (1u << (K * kChunks)) - 1u)) return;
         for (int i = 0; i < stages * R * count * K; ++i) {
 #pragma unroll
             for (int c = 0; c < kChunks; ++c)
                 asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};"
-                             :: "r"(ring + i * region + copy_base + c * copy_step), "r"(0u) : "memory");
+                             :: "r"(ring + i * kBlock + (threadIdx.x & 31) * 16 + c * 512), "r"(0u) : "memory");
         }
         __syncwarp();
     }
-    // Copies the rows `turns` turns of R rows from these into the ring's stage at `to` (and
-    // the single elements to end_w[stage]), as one group of asynchronous copies with what was
-    // issued since the last.
+    // Copies the next R rows into the stage at `to` of this warp's ring (and the single elements
+    // to end_w[stage]), as one group of asynchronous copies with what was issued since the last.
     template <int OPS, class Ends>
-    __device__ __forceinline__ void issue(uint32_t to, int stage, int turns, const char *const (&ops)[OPS],
-                                          int count, Ends &end_w) const {
+    __device__ __forceinline__ void issue(uint32_t to, int stage, const char *const (&ops)[OPS], int count,
+                                          Ends &end_w) {
 #pragma unroll
         for (int rr = 0; rr < R; ++rr) {
-            if (turns * R + rr < left) {
-                const int64_t row_at = at + (turns * R + rr) * step;
+            if (rr < copy_left) {
+                const int64_t row_at = copy_at + rr * step;
 #pragma unroll
                 for (int o = 0; o < OPS; ++o) {
                     if (o >= count) break;
-                    const char *src = ops[o] + (row_at + copy_off);
-                    const uint32_t dst = to + (rr * count + o) * K * region + copy_base;
+                    const char *src = ops[o] + row_at;
+                    const uint32_t dst = to + (rr * count + o) * K * kBlock + copy_to;
 #pragma unroll
                     for (int k = 0; k < K; ++k) {
 #pragma unroll
-                        for (int c = 0; c < kChunks; ++c)
-                            cp_async16_if(copies & (1u << (k * kChunks + c)), dst + k * region + c * copy_step,
-                                          src + k * (width * 8 * T::kBytes) + c * copy_step);
+                        for (int c = 0; c < kChunks; ++c) {
+                            const int i = k * kChunks + c;
+                            cp_async16_if(copies & (1u << i),
+                                          dst + k * kBlock + (WARP ? c * lanes * 16 : c * 512),
+                                          src + (WARP ? i * lanes * 16 : i * 512));
+                        }
                     }
                 }
                 if (EDGE && ends) {
                     if (end_col >= 0) {
-                        const int64_t e = row_at + (end_col - before) * T::kBytes;
+                        // (the row's slot 0, from this thread's first chunk)
+                        const int li = WARP ? first : static_cast<int>(threadIdx.x & 31);
+                        const int64_t e = row_at - ((first - li) * kChunks + li) * 16 + (end_col - before) * T::kBytes;
 #pragma unroll
                         for (int o = 0; o < OPS; ++o) {
                             if (o >= count) break;
@@ -285,13 +299,15 @@ template <class T, int K, int R, bool EDGE, bool WARP> struct RowTile {
                 }
             }
         }
+        copy_at += R * step;
+        copy_left -= R;
         cp_async_commit();
     }
     // This thread's slots of operand o of row rr in the stage at `from`, zero outside the row.
     __device__ __forceinline__ void fetch(Slot<T> (&s)[K], uint32_t from, int o, int rr, int count) const {
-        const uint32_t src = from + (rr * count + o) * K * region + slot_base;
+        const uint32_t src = from + (rr * count + o) * K * kBlock + slot_from;
 #pragma unroll
-        for (int k = 0; k < K; ++k) ld_shared_slot(s[k], src + k * region);
+        for (int k = 0; k < K; ++k) ld_shared_slot(s[k], src + k * kBlock);
         if constexpr (WARP || R > 1) {
             if (!valid(rr)) {      // (past the last row: the stage holds an earlier one)
 #pragma unroll
@@ -314,7 +330,7 @@ template <class T, int K, int R, bool EDGE, bool WARP> struct RowTile {
         char *p = base + at + rr * step + first * (8 * T::kBytes);
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            st_slot_if(on && holds(k), p + k * (width * 8 * T::kBytes), s[k]);
+            st_slot_if(on && holds(k), p + k * slot_step() * (8 * T::kBytes), s[k]);
     }
     // Stores this thread's single element; returns it as stored.
     __device__ __forceinline__ float store_end(char *base, int rr, bool on, float v) const {
@@ -327,7 +343,7 @@ template <class T, int K, int R, bool EDGE, bool WARP> struct RowTile {
     // Generator group of slot k (the operands start on a slot boundary), and the element number
     // of the single element.
     __device__ __forceinline__ uint64_t group(int rr, int k) const {
-        return static_cast<uint64_t>(at + rr * step) / (8 * T::kBytes) + static_cast<uint64_t>(first + k * width);
+        return static_cast<uint64_t>(at + rr * step) / (8 * T::kBytes) + static_cast<uint64_t>(first + k * slot_step());
     }
     __device__ __forceinline__ int64_t end_element(int rr) const {
         return (at + rr * step) / T::kBytes + end_col - before;

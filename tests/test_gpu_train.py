@@ -15,10 +15,17 @@ SEED, OFFSET, SITE = -0x123456789ABCDEF, 0x7FFFFFFFFFFFFFF0, 21   # the step's l
 GUARD = 64
 
 # rows x n: one and two elements, lanes, warps and CTAs left partly idle, odd widths, widths
-# of the benchmark, rows wider than any register tile, more rows than CTAs
+# of the benchmark, rows over clusters of CTAs and wider than any register tile
 SHAPES = [(1, 1), (3, 2), (5, 7), (2, 31), (9, 32), (65, 33), (3, 127), (1300, 64), (700, 130),
           (33, 255), (64, 768), (7, 1023), (33, 1024), (160, 2049), (5, 4096), (4, 4097),
-          (3, 6655), (4, 6656), (2, 8200), (3, 16384), (2, 20001), (1, 40000), (2, 70000)]
+          (3, 6655), (4, 6656), (2, 8200), (3, 16384), (2, 20001), (1, 40000), (2, 70000),
+          (1, 131080), (2, 140001), (1, 270001)]
+# more rows than SMs: every number of slots per thread and of rows at a time, several turns of a
+# CTA and a last one that is not full, one warp and several warps to a row, clusters
+SHAPES += [(9999, 3), (5000, 8), (3001, 15), (2500, 100), (1301, 257), (1000, 769), (1001, 1025),
+           (333, 1535), (1250, 1544), (700, 3001), (613, 4095), (620, 4096), (457, 5121),
+           (461, 6655), (470, 6656), (320, 8191), (161, 12296), (155, 16391), (159, 33000),
+           (153, 65544)]
 
 
 @pytest.fixture(scope="module", autouse=True)
