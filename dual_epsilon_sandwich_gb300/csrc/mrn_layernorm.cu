@@ -205,14 +205,12 @@ bool launch_layernorm_tile(const LayernormArgs &a, const TileShape &p, int sms, 
     static TileLaunchCache cache;
     const auto fn = mrn_layernorm_tile_kernel<T, K, R, EDGE, WARP, ADD>;
     constexpr int kOps = ADD ? 2 : 1;
-    int resident = 0;
-    *err = open_tile(cache, fn, p.threads, &resident);
+    TileGrid g;
+    *err = tile_grid(cache, fn, p, a.rows, a.n, R, T::kBytes, kOps, 32, sms, &g);
     if (*err != cudaSuccess) return true;
-    const TileGrid g = tile_grid(p, a.rows, R, T::kBytes, kOps, resident, 32, sms);
     if (g.stages < 1) return false;
     const TileArgs t = {p.lanes, g.stages, p.mis, a.stall};
-    *err = launch_tile(fn, p, g.ctas, tile_ring_bytes(T::kBytes, K, p.threads, g.stages, kOps * R), pdl,
-                       stream, launches, a, t);
+    *err = launch_tile(fn, p, g.ctas, g.shared, pdl, stream, launches, a, t);
     return true;
 }
 
@@ -268,7 +266,6 @@ cudaError_t launch_layernorm_typed(const LayernormArgs &a, int sms, bool pdl, cu
         int k = 4, r = 1, most_threads = 0;
         forward_tile<T>(a.n / 8, a.res != nullptr, mis != 0 || a.n % 8 != 0, &k, &r, &most_threads);
         if (most_threads == 0 || most_threads > forward_threads<T>(k, r)) most_threads = forward_threads<T>(k, r);
-        //KR
         const bool few = tile_few_rows(a.rows, a.n, sms);
         if (few) {
             k = r = 1;
@@ -283,7 +280,6 @@ cudaError_t launch_layernorm_typed(const LayernormArgs &a, int sms, bool pdl, cu
                    : p.k == 3 ? launch_layernorm_k<T, 3, 1, true>(a, p, sms, pdl, stream, launches, &err)
                               : launch_layernorm_k<T, 4, 1, true>(a, p, sms, pdl, stream, launches, &err);
         } else if (p.ok) {
-            //MORE
             if (k == 1) done = launch_layernorm_k<T, 1, 1, false>(a, p, sms, pdl, stream, launches, &err);
             else if (T::kBytes == 4 && k == 2 && r == 1) done = launch_layernorm_k<T, 2, 1, false>(a, p, sms, pdl, stream, launches, &err);
             else if (k == 2) done = launch_layernorm_k<T, 2, 2, false>(a, p, sms, pdl, stream, launches, &err);

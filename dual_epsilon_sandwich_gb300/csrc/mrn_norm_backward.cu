@@ -340,17 +340,15 @@ bool launch_backward_tile(const BackwardArgs &a, const TileShape &p, BackwardLau
     static TileLaunchCache cache;
     const auto fn = mrn_norm_backward_tile_kernel<T, K, EDGE, WARP, RMS>;
     const int operands = a.dstream ? 3 : 2;
-    int resident = 0;
-    l.err = open_tile(cache, fn, p.threads, &resident);
+    TileGrid g;
+    l.err = tile_grid(cache, fn, p, a.rows, a.n, 1, T::kBytes, operands, kPartsPerSm, l.sms, &g);
     if (l.err != cudaSuccess) return true;
-    const TileGrid g = tile_grid(p, a.rows, 1, T::kBytes, operands, resident, kPartsPerSm, l.sms);
     l.parts = g.ctas / p.cluster;
     if (g.stages < 1 || l.parts > l.most_parts) return false;   // (the workspace holds no more)
     const TileArgs t = {p.lanes, g.stages, p.mis, a.stall};
     const int64_t stride = part_stride_of(a.n);
     // (WARP: the epilogue's rows have room for the ends)
-    const int64_t shared = tile_ring_bytes(T::kBytes, K, p.threads, g.stages, operands) + (WARP ? 1024 : 0);
-    l.err = launch_tile(fn, p, g.ctas, shared,
+    l.err = launch_tile(fn, p, g.ctas, g.shared + (WARP ? 1024 : 0),
                         l.pdl, l.stream, l.launches, a, t, a.workspace,
                         a.dbeta ? a.workspace + l.parts * stride : nullptr, stride);
     return true;
@@ -377,9 +375,8 @@ struct JoinArgs {
     int mis;
     bool shifted;
 };
-constexpr int kJoinFlight = 8;
 
-template <int WARPS, int C>
+template <int WARPS, int C, int kJoinFlight>
 __global__ void __launch_bounds__(WARPS * 32) mrn_norm_backward_join_kernel(const JoinArgs a) {
     __shared__ float sums[WARPS][C * 32];
     pdl_enter();
@@ -418,7 +415,7 @@ __global__ void __launch_bounds__(WARPS * 32) mrn_norm_backward_join_kernel(cons
     }
 }
 
-template <int WARPS, int C>
+template <int WARPS, int C, int FLIGHT>
 cudaError_t launch_join_typed(const JoinArgs &a, bool pdl, cudaStream_t stream, uint64_t *launches) {
     const int64_t ctas = (a.n + 32 * C - 1) / (32 * C);
     if (ctas > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
@@ -433,7 +430,7 @@ cudaError_t launch_join_typed(const JoinArgs &a, bool pdl, cudaStream_t stream, 
         cfg.attrs = attr;
         cfg.numAttrs = 1;
     }
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, mrn_norm_backward_join_kernel<WARPS, C>, a);
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, mrn_norm_backward_join_kernel<WARPS, C, FLIGHT>, a);
     if (err == cudaSuccess) ++*launches;
     return err;
 }
@@ -441,8 +438,8 @@ cudaError_t launch_join_typed(const JoinArgs &a, bool pdl, cudaStream_t stream, 
 cudaError_t launch_join(const JoinArgs &a, bool pdl, cudaStream_t stream, uint64_t *launches) {
     // (measured on GB300, us a call: 163840 x 128 bf16, 1216 partial rows, 25.3 with 32 warps
     // of 32 columns against 27.2 with 16 of 64; 16384 x 4096 bf16 71.2 against 70.0)
-    return a.n <= 1024 ? launch_join_typed<32, 1>(a, pdl, stream, launches)
-                       : launch_join_typed<16, 2>(a, pdl, stream, launches);
+    return a.n <= 1024 ? launch_join_typed<32, 1, 20>(a, pdl, stream, launches)
+                       : launch_join_typed<16, 2, 10>(a, pdl, stream, launches);
 }
 
 template <class T>
@@ -470,7 +467,6 @@ cudaError_t launch_backward_typed(const BackwardArgs &a, int sms, bool pdl, cuda
         int most_threads = backward_resident(k);
         if (T::kBytes == 4 && k == 2 && slots <= 8192) most_threads = 256;
         if (T::kBytes == 2 && k == 4) most_threads = slots <= 2048 ? 64 : (slots <= 4096 ? 128 : 256);
-        //KR
         const bool few = tile_few_rows(a.rows, a.n, sms);
         if (few) {
             k = 1;
@@ -483,7 +479,6 @@ cudaError_t launch_backward_typed(const BackwardArgs &a, int sms, bool pdl, cuda
                    : p.k == 3 ? launch_backward_k<T, 3, true>(a, p, l)
                               : launch_backward_k<T, 4, true>(a, p, l);
         } else if (p.ok) {
-            //MORE
             constexpr int kOther = T::kBytes == 2 ? 4 : 3;
             done = k == 1   ? launch_backward_k<T, 1, false>(a, p, l)
                    : k == 2 ? launch_backward_k<T, 2, false>(a, p, l)

@@ -74,7 +74,7 @@ __device__ __forceinline__ void ld_shared_slot(Slot<F32> &s, uint32_t p) {
 // every peer as st.async messages, which land in the peer's box for this turn and complete
 // the peer's mbarrier for it; a CTA waits for its own and adds the sums in rank order (all
 // CTAs get the same bits).  A cluster barrier instead would make each row wait for the
-// stores of the row before it (16384 f32: 193 us against %CLUSTER% us for the gradient of
+// stores of the row before it (16384 f32: 193 us against 178 for the gradient of
 // 4096 rows).  Boxes and mbarriers alternate: a CTA sends turn t + 2 only after it has every
 // peer's t + 1, which a peer sends only after all its threads have read t.
 template <int N> struct RowSumSlots {
@@ -494,36 +494,6 @@ inline TileShape tile_shape(int64_t n, int mis, int k, int most_threads, bool fe
     return s;
 }
 
-// The rest of a launch: as many CTAs as the registers let an SM hold, a ring as deep as
-// shared memory then allows (two stages at least where it can be), and a persistent grid.
-struct TileGrid {
-    int stages;       // 0: the ring does not fit
-    int64_t ctas;
-};
-
-inline TileGrid tile_grid(const TileShape &s, int64_t rows, int rows_at_a_time, int elem_bytes, int operands,
-                          int resident, int most_ctas_per_sm, int sms) {
-    TileGrid g = {};
-    int per_sm = resident < most_ctas_per_sm ? resident : most_ctas_per_sm;
-    const int64_t stage = tile_ring_bytes(elem_bytes, s.k, s.threads, 1, operands * rows_at_a_time);
-    for (;; --per_sm) {
-        const int64_t budget = (kTileSharedBudget - (per_sm - 1) * kTileStaticShared) / per_sm;
-        g.stages = static_cast<int>(budget / stage);
-        if (g.stages >= 2 || per_sm == 1) break;
-    }
-    //TUNE
-    if (g.stages > kTileMaxStages) g.stages = kTileMaxStages;
-    const int64_t rows_per_cta = s.warp ? s.threads / s.lanes : 1;
-    int64_t groups = static_cast<int64_t>(sms) * per_sm / s.cluster;      // CTAs or clusters
-    // rows of one CTA start alike only when they are a multiple of eight apart
-    if (groups > 8) groups -= groups % 8;
-    if (groups < 8) groups = 8;
-    const int64_t need = (rows + rows_per_cta - 1) / rows_per_cta;
-    if (groups > need) groups = need;
-    g.ctas = groups * s.cluster;
-    return g;
-}
-
 // Elements from the slot boundary below a row operand to its base; -1 when the
 // operands (NULL: none) do not share it.
 template <class... P> inline int common_offset(int elem_bytes, const void *first, P... rest) {
@@ -534,12 +504,14 @@ template <class... P> inline int common_offset(int elem_bytes, const void *first
     return static_cast<int>(at) / elem_bytes;
 }
 
-// What is known of a kernel on each device: the CTAs that an SM's registers hold at the
-// last number of threads asked for (threads * 64 + CTAs; 0 until the kernel has been opened to
-// the shared memory and the cluster sizes below).  Every thread finds the same values, so
-// that calls that race only repeat them.
+// What is known of a kernel on each device: the CTAs that an SM's registers hold at the last
+// number of threads asked for (threads * 64 + CTAs; 0 until the kernel has been opened to
+// the shared memory and the cluster sizes below), and the clusters that the device holds at
+// the last (threads, cluster, shared memory).  Every thread finds the same values, so that calls
+// that race only repeat them.
 struct TileLaunchCache {
     std::atomic<int> resident[kMaxCachedDevices];
+    std::atomic<uint64_t> clusters[kMaxCachedDevices];
 };
 
 template <class... Params>
@@ -564,6 +536,86 @@ cudaError_t open_tile(TileLaunchCache &cache, void (*fn)(Params...), int threads
     if (err != cudaSuccess) return err;
     if (*resident < 1) return cudaErrorInvalidConfiguration;
     if (cached) cache.resident[dev].store(threads * 64 + *resident, std::memory_order_release);
+    return cudaSuccess;
+}
+
+// Clusters of p.cluster CTAs that the device holds at once: fewer than its SMs divided by their
+// number, since a cluster does not leave its group of SMs; a grid of more would end in a second
+// wave (4096 x 16384 f32, the gradient of RMSNorm: 256 us against 180).
+template <class... Params>
+cudaError_t resident_clusters(TileLaunchCache &cache, void (*fn)(Params...), const TileShape &p, int64_t shared,
+                              int *count) {
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const bool cached = dev >= 0 && dev < kMaxCachedDevices;
+    const uint64_t key = (static_cast<uint64_t>(shared) * 2048 + p.threads) * 32 + p.cluster;
+    const uint64_t known = cached ? cache.clusters[dev].load(std::memory_order_relaxed) : 0;
+    if (known / 4096 == key) {
+        *count = static_cast<int>(known % 4096);
+        return cudaSuccess;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(p.cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(p.cluster), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(p.threads), 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(shared);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    err = cudaOccupancyMaxActiveClusters(count, fn, &cfg);
+    if (err != cudaSuccess) return err;
+    if (*count < 1) return cudaErrorInvalidConfiguration;
+    if (*count > 4095) *count = 4095;
+    if (cached) cache.clusters[dev].store(key * 4096 + *count, std::memory_order_relaxed);
+    return cudaSuccess;
+}
+
+// The rest of a launch: as many CTAs as the registers let an SM hold (at most most_per_sm), a
+// ring as deep as shared memory then allows (two stages at least where it can be), and a
+// persistent grid.
+struct TileGrid {
+    int stages;       // 0: the ring does not fit
+    int64_t ctas;
+    int64_t shared;   // bytes of the ring
+};
+
+template <class... Params>
+cudaError_t tile_grid(TileLaunchCache &cache, void (*fn)(Params...), const TileShape &s, int64_t rows, int64_t n,
+                      int rows_at_a_time, int elem_bytes, int operands, int most_per_sm, int sms, TileGrid *g) {
+    *g = TileGrid{};
+    int per_sm = 0;
+    cudaError_t err = open_tile(cache, fn, s.threads, &per_sm);
+    if (err != cudaSuccess) return err;
+    if (per_sm > most_per_sm) per_sm = most_per_sm;
+    const int64_t stage = tile_ring_bytes(elem_bytes, s.k, s.threads, 1, operands * rows_at_a_time);
+    for (;; --per_sm) {
+        const int64_t budget = (kTileSharedBudget - (per_sm - 1) * kTileStaticShared) / per_sm;
+        g->stages = static_cast<int>(budget / stage);
+        if (g->stages >= 2 || per_sm == 1) break;
+    }
+    if (g->stages > kTileMaxStages) g->stages = kTileMaxStages;
+    if (g->stages < 1) return cudaSuccess;
+    g->shared = stage * g->stages;
+    int64_t groups = static_cast<int64_t>(sms) * per_sm;      // CTAs or clusters
+    if (s.cluster > 1) {
+        int clusters = 0;
+        err = resident_clusters(cache, fn, s, g->shared, &clusters);
+        if (err != cudaSuccess) return err;
+        const int64_t most = static_cast<int64_t>(sms) * most_per_sm / s.cluster;
+        groups = clusters < most ? clusters : most;
+    }
+    const int64_t rows_per_cta = s.warp ? s.threads / s.lanes : 1;
+    // rows of one CTA start alike only when they are a multiple of eight elements apart
+    int64_t alike = 1;
+    while (alike * rows_per_cta % 8 * (n % 8) % 8 != 0) alike *= 2;
+    groups = groups < alike ? alike : groups - groups % alike;
+    const int64_t need = (rows + rows_per_cta - 1) / rows_per_cta;
+    if (groups > need) groups = need;
+    g->ctas = groups * s.cluster;
     return cudaSuccess;
 }
 
