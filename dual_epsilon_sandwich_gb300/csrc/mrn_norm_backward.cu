@@ -205,18 +205,21 @@ mrn_norm_backward_tile_kernel(const BackwardArgs a, const TileArgs t, float *par
         if (RMS) {
             rstd = inv_sqrt(fmaf(s[0], inv_n, a.eps));
             scale = f2_pack(rstd, rstd);
-            c2 = -(s[1] * inv_n * rstd) * rstd * rstd;
-            // dy once more, for dgamma
+            s[1] *= rstd;
+            // xh itself, and dy once more for dgamma
             tile.fetch(dy, from, 0, 0, ops_count);
 #pragma unroll
             for (int k = 0; k < K; ++k)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    sum_g[k][i] = f2_fma(dy[k].pair(i), f2_mul(xh[k][i], scale), sum_g[k][i]);
+                for (int i = 0; i < 4; ++i) {
+                    xh[k][i] = f2_mul(xh[k][i], scale);
+                    sum_g[k][i] = f2_fma(dy[k].pair(i), xh[k][i], sum_g[k][i]);
+                }
+            end_xh *= rstd;
         } else {
             c1 = -(s[0] * inv_n) * rstd;
-            c2 = -(s[1] * inv_n) * rstd;
         }
+        c2 = -(s[1] * inv_n) * rstd;
         const uint64_t c1p = f2_pack(c1, c1), c2p = f2_pack(c2, c2);
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -239,7 +242,7 @@ mrn_norm_backward_tile_kernel(const BackwardArgs a, const TileArgs t, float *par
         if (EDGE && tile.ends) {
             const float ew = end_d * end_gamma;
             float o = fmaf(end_xh, c2, RMS ? ew * rstd : fmaf(ew, rstd, c1));
-            if (RMS) end_sum_g = fmaf(end_d, end_xh * rstd, end_sum_g);
+            if (RMS) end_sum_g = fmaf(end_d, end_xh, end_sum_g);
             if (a.dstream) o += tile.fetch_end(end_w, walk.read, 2, 0);
             end_o = o;
             tile.store_end(a.dres ? dres : dx, 0, ok, o);

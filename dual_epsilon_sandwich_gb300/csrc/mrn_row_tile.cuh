@@ -27,7 +27,7 @@
 namespace mrn {
 
 struct TileArgs {
-    int lanes;      // threads per row when several rows share a warp (WARP); else unused
+    int lanes;      // threads per row when rows share a warp (WARP); else unused
     int stages;     // ring depth
     int mis;        // elements from the slot boundary below the operands' base to the base
     uint32_t stall; // see row_sum
@@ -35,7 +35,6 @@ struct TileArgs {
 
 constexpr int kTileMaxThreads = 512;
 constexpr int kTileMaxStages = 4;
-constexpr int kTileMaxOperands = 3;
 
 // 16 bytes to shared memory when `on` is not 0 (predicated, no branch).
 __device__ __forceinline__ void cp_async16_if(uint32_t on, uint32_t dst, const void *src) {
@@ -485,8 +484,8 @@ inline TileShape tile_shape(int64_t n, int mis, int k, int most_threads, bool fe
     } else {
         s.k = k;
         const int64_t most = int64_t(k) * most_threads;
+        if (slots > most * kMaxCluster) return s;
         s.cluster = static_cast<int>((slots + most - 1) / most);
-        if (s.cluster > kMaxCluster) return s;
         const int64_t per = (slots + s.cluster - 1) / s.cluster;
         s.threads = static_cast<int>((per + 32 * k - 1) / (32 * k)) * 32;
     }
@@ -504,14 +503,15 @@ template <class... P> inline int common_offset(int elem_bytes, const void *first
     return static_cast<int>(at) / elem_bytes;
 }
 
-// What is known of a kernel on each device: the CTAs that an SM's registers hold at the last
-// number of threads asked for (threads * 64 + CTAs; 0 until the kernel has been opened to
-// the shared memory and the cluster sizes below), and the clusters that the device holds at
-// the last (threads, cluster, shared memory).  Every thread finds the same values, so that calls
-// that race only repeat them.
+// What is known of a kernel on each device: the CTAs that an SM's registers hold, by the warps
+// of a CTA (0: not asked yet, and entry 0 whether the kernel has been opened to the shared
+// memory and the cluster sizes below), and the clusters that the device holds, in a few
+// entries of (threads, cluster, shared memory).  Every thread finds the same values, so that
+// calls that race only repeat them.
+constexpr int kClusterEntries = 8;
 struct TileLaunchCache {
-    std::atomic<int> resident[kMaxCachedDevices];
-    std::atomic<uint64_t> clusters[kMaxCachedDevices];
+    std::atomic<int> resident[kMaxCachedDevices][kTileMaxThreads / 32 + 1];
+    std::atomic<uint64_t> clusters[kMaxCachedDevices][kClusterEntries];
 };
 
 template <class... Params>
@@ -520,10 +520,9 @@ cudaError_t open_tile(TileLaunchCache &cache, void (*fn)(Params...), int threads
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
     const bool cached = dev >= 0 && dev < kMaxCachedDevices;
-    const int known = cached ? cache.resident[dev].load(std::memory_order_acquire) : 0;
-    *resident = known % 64;
-    if (known / 64 == threads) return cudaSuccess;
-    if (known == 0) {
+    *resident = cached ? cache.resident[dev][threads / 32].load(std::memory_order_acquire) : 0;
+    if (*resident > 0) return cudaSuccess;
+    if (!cached || cache.resident[dev][0].load(std::memory_order_acquire) == 0) {
         err = cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    static_cast<int>(kTileSharedBudget));
@@ -531,11 +530,12 @@ cudaError_t open_tile(TileLaunchCache &cache, void (*fn)(Params...), int threads
         err = cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
                                    cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (err != cudaSuccess) return err;
+        if (cached) cache.resident[dev][0].store(1, std::memory_order_release);
     }
     err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(resident, fn, threads, 0);
     if (err != cudaSuccess) return err;
     if (*resident < 1) return cudaErrorInvalidConfiguration;
-    if (cached) cache.resident[dev].store(threads * 64 + *resident, std::memory_order_release);
+    if (cached) cache.resident[dev][threads / 32].store(*resident, std::memory_order_release);
     return cudaSuccess;
 }
 
@@ -550,7 +550,9 @@ cudaError_t resident_clusters(TileLaunchCache &cache, void (*fn)(Params...), con
     if (err != cudaSuccess) return err;
     const bool cached = dev >= 0 && dev < kMaxCachedDevices;
     const uint64_t key = (static_cast<uint64_t>(shared) * 2048 + p.threads) * 32 + p.cluster;
-    const uint64_t known = cached ? cache.clusters[dev].load(std::memory_order_relaxed) : 0;
+    std::atomic<uint64_t> &entry = cache.clusters[cached ? dev : 0][key * 0x9E3779B97F4A7C15u >> 61];
+    static_assert(kClusterEntries == 8, "three bits of the hash");
+    const uint64_t known = cached ? entry.load(std::memory_order_relaxed) : 0;
     if (known / 4096 == key) {
         *count = static_cast<int>(known % 4096);
         return cudaSuccess;
@@ -570,7 +572,7 @@ cudaError_t resident_clusters(TileLaunchCache &cache, void (*fn)(Params...), con
     if (err != cudaSuccess) return err;
     if (*count < 1) return cudaErrorInvalidConfiguration;
     if (*count > 4095) *count = 4095;
-    if (cached) cache.clusters[dev].store(key * 4096 + *count, std::memory_order_relaxed);
+    if (cached) entry.store(key * 4096 + *count, std::memory_order_relaxed);
     return cudaSuccess;
 }
 

@@ -236,6 +236,32 @@ def test_unusual_rows(n, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", (1, 33, 1024, 4097, 20001))
+@pytest.mark.parametrize("kind", ("ln", "rms"))
+def test_gradients_of_unusual_rows(kind, n, dtype):
+    """The same rows, and incoming gradients of zero."""
+    x, dy = make(18, 7, n, dtype), make(19, 7, n, dtype)
+    x[0], x[1] = 3.0, 0.0
+    x[2] = (x[2].float() + 1000.0).to(x.dtype)
+    x[3] = (x[3].float() * 1e-15).to(x.dtype)
+    x[4] = (x[4].float() * 1e17).to(x.dtype)
+    dy[5] = 0.0
+    gamma, _ = weights(20, n, dtype)
+    mean, rstd = device_stats(x)
+    dx, _, dg, db = run_backward(kind, dy, x, gamma, mean, rstd, None, dtype)
+    if kind == "rms":
+        (wx, wg), (tx, tg) = ref.rmsnorm_backward(f64(dy), f64(x), f64(gamma),
+                                                  float(np.float32(1e-5)))
+    else:
+        (wx, wg, wb), (tx, tg, tb) = ref.layernorm_backward(f64(dy), f64(x), f64(gamma), f64(mean),
+                                                            f64(rstd))
+        ref.check(f64(db), wb, tb, "f32", "dbeta")
+    ref.check(f64(dx), wx, tx, dtype, "dx")
+    ref.check(f64(dg), wg, tg, "f32", "dgamma")
+    assert not f64(dx)[5].any()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("n", (5, 1024, 4097))
 def test_infinities_stay_in_their_rows(n, dtype):
     rows = 7
@@ -278,7 +304,8 @@ def test_dropped_values_do_not_reach_the_result(n, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("rows,n", [(5, 33), (40, 1023), (700, 512), (3, 20001)])
+@pytest.mark.parametrize("rows,n", [(5, 33), (40, 1023), (700, 512), (3, 20001), (1501, 1023),
+                                    (2000, 99)])
 def test_in_place(rows, n, dtype):
     """Every output that may be one of the row inputs gives the bits it gives elsewhere."""
     t = TYPES[dtype]
@@ -571,3 +598,138 @@ def test_launches_are_counted():
     mrn.layernorm(x, g, g, 1e-5)
     mrn.dropout_add(x, x, 0.1, rng_tensor())
     assert mrn.mrn_launch_count() == before + 2
+
+
+def test_elements_past_32_bits():
+    """More than 2^31 elements: the last rows give what they give alone, and their masks are
+    those of their element numbers."""
+    rows, n, p = 70001, 32771, 0.25
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB of device memory")
+    x = torch.empty(rows, n, dtype=torch.bfloat16, device="cuda")
+    x.normal_(generator=torch.Generator(device="cuda").manual_seed(90))
+    gamma, beta = (w.cuda() for w in weights(91, n, "bf16"))
+    mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    out = mrn.layernorm(x, gamma, beta, 1e-5, mean=mean, rstd=rstd)
+    alone = f64(mrn.layernorm(x[-200:].clone(), gamma, beta, 1e-5))
+    # (another grid may take the sums in another order)
+    (_, _, _), (tol, _, _) = ref.layernorm(f64(x[-200:]), f64(gamma), f64(beta), 1e-5)
+    ref.check(f64(out[-200:]), alone, 2 * tol + ref.HALF["bf16"] * np.abs(alone), "bf16", "last rows")
+    mrn.dropout_add(x, None, p, rng_tensor(), site=SITE, out=out)
+    first = (rows - 2) * n // 8
+    words = ref.philox_words(SEED & (2 ** 64 - 1), (OFFSET + SITE) & (2 ** 64 - 1),
+                             np.arange(first, (rows * n + 7) // 8))
+    lanes = np.stack([v for w in words for v in (w & np.uint64(0xFFFF), w >> np.uint64(16))], 1)
+    keep = (lanes.reshape(-1) >= ref.threshold(p))[(rows - 2) * n - first * 8:][:2 * n]
+    got = f64(out[-2:]).reshape(-1)
+    assert not got[~keep].any()
+    want = f64(x[-2:]).reshape(-1) * ref.drop_scale(p)
+    ref.check(got[keep], want[keep], 2 * ref.U * np.abs(want[keep]), "bf16", "last rows kept")
+    # the gradient's last rows: dx from their own statistics
+    dx, _, _ = mrn.layernorm_backward(x, x, gamma, mean, rstd, dx=out)
+    (want, _, _), (tol, _, _) = ref.layernorm_backward(
+        f64(x[-3:]), f64(x[-3:]), f64(gamma), f64(mean[-3:]), f64(rstd[-3:]))
+    ref.check(f64(dx[-3:]), want, tol, "bf16", "dx of the last rows")
+
+
+def test_graphs_that_share_a_workspace():
+    """Two captured gradients with one workspace, replayed one after the other on one stream."""
+    shapes = [(300, 1000), (2000, 257)]
+    x = [make(92 + i, r, n, "f32").cuda() for i, (r, n) in enumerate(shapes)]
+    dy = [make(94 + i, r, n, "f32").cuda() for i, (r, n) in enumerate(shapes)]
+    gamma = [weights(96 + i, n, "f32")[0].cuda() for i, (_, n) in enumerate(shapes)]
+    ws = max((mrn.norm_backward_workspace(t) for t in x), key=lambda t: t.numel())
+    want = [mrn.rmsnorm_backward(dy[i], x[i], gamma[i], 1e-5, workspace=ws) for i in range(2)]
+    want = [[t.clone() for t in w] for w in want]
+    graphs, outs = [], []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(mrn.rmsnorm_backward(dy[i], x[i], gamma[i], 1e-5, workspace=ws))
+        graphs.append(g)
+    ws.fill_(255)                        # NaN: nothing of an earlier call may be read
+    for i in (0, 1, 1, 0, 0, 1):
+        for t in outs[i]:
+            t.fill_(float("nan"))
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs[i], want[i])), i
+
+
+def test_a_large_enough_workspace_serves_smaller_calls():
+    x = make(98, 2000, 1000, "bf16").cuda()
+    ws = mrn.norm_backward_workspace(x)
+    small = x[:50].contiguous()
+    gamma = torch.ones(1000, dtype=torch.bfloat16, device="cuda")
+    a = mrn.rmsnorm_backward(small, small, gamma, 1e-5, workspace=ws)
+    b = mrn.rmsnorm_backward(small, small, gamma, 1e-5)
+    assert all(torch.equal(u, v) for u, v in zip(a, b))
+    with pytest.raises(mrn.MrnError):
+        mrn.rmsnorm_backward(x, x, gamma, 1e-5, workspace=mrn.norm_backward_workspace(small))
+
+
+def test_unsigned_generator_state():
+    x = torch.ones(16, 64, device="cuda")
+    signed = rng_tensor(-5, -9)
+    assert torch.equal(mrn.dropout_add(x, None, 0.5, signed),
+                       mrn.dropout_add(x, None, 0.5, signed.view(torch.uint64)))
+
+
+def test_threads_calling_at_once():
+    """First calls of a shape from several threads, each on its own stream."""
+    import threading
+    rows, n = 500, 1411
+    x = [make(100 + i, rows, n, "bf16").cuda() for i in range(4)]
+    gamma, beta = (w.cuda() for w in weights(104, n, "bf16"))
+    torch.cuda.synchronize()
+    got = [None] * 4
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+            y = mrn.layernorm(x[i], gamma, beta, 1e-5, mean=mean, rstd=rstd)
+            got[i] = (y, *mrn.layernorm_backward(x[i], x[i], gamma, mean, rstd))
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(4):
+        mean, rstd = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+        y = mrn.layernorm(x[i], gamma, beta, 1e-5, mean=mean, rstd=rstd)
+        want = (y, *mrn.layernorm_backward(x[i], x[i], gamma, mean, rstd))
+        assert all(torch.equal(a, b) for a, b in zip(got[i], want)), i
+
+
+def test_a_cluster_whose_messages_are_late_stops_and_recovers():
+    """The launch option that makes the first wait of a cluster expect bytes that never come:
+    the calls return, the kernels stop after about a second, mrn_wait_timeouts() reports them,
+    and the next calls are exact."""
+    import time
+    rows, n = 3, 16384
+    x, dy = make(110, rows, n, "f32"), make(111, rows, n, "f32")
+    gamma, beta = weights(112, n, "f32")
+    mean, rstd = device_stats(x)
+    xd, dyd, gd, bd = x.cuda(), dy.cuda(), gamma.cuda(), beta.cuda()
+    assert mrn.mrn_wait_timeouts() == 0
+    torch.cuda.synchronize()
+    assert mrn.mrn_set_launch_options(mrn.MRN_LAUNCH_PDL | mrn.MRN_LAUNCH_TEST_WAIT_TIMEOUT) == 0
+    try:
+        t0 = time.perf_counter()
+        mrn.layernorm(xd, gd, bd, 1e-5)
+        mrn.layernorm_backward(dyd, xd, gd, mean, rstd)
+        torch.cuda.synchronize()
+        seconds = time.perf_counter() - t0
+    finally:
+        mrn.mrn_set_launch_options(mrn.MRN_LAUNCH_PDL)
+    assert mrn.mrn_wait_timeouts() >= 2 and seconds < 30, seconds
+    got = run_layernorm(x, gamma, beta, 1e-5, "f32")
+    check_layernorm(got, x, gamma, beta, 1e-5, "f32", "after a timeout")
+    dx, _, dg, _ = run_backward("ln", dy, x, gamma, mean, rstd, None, "f32")
+    (wx, wg, _), (tx, tg, _) = ref.layernorm_backward(f64(dy), f64(x), f64(gamma), f64(mean),
+                                                      f64(rstd))
+    ref.check(f64(dx), wx, tx, "f32", "dx after a timeout")
+    ref.check(f64(dg), wg, tg, "f32", "dgamma after a timeout")
+    assert mrn.mrn_wait_timeouts() == 0
