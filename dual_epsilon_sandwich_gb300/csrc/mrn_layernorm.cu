@@ -280,10 +280,18 @@ cudaError_t launch_layernorm_typed(const LayernormArgs &a, int sms, bool pdl, cu
                    : p.k == 3 ? launch_layernorm_k<T, 3, 1, true>(a, p, sms, pdl, stream, launches, &err)
                               : launch_layernorm_k<T, 4, 1, true>(a, p, sms, pdl, stream, launches, &err);
         } else if (p.ok) {
-            if (k == 1) done = launch_layernorm_k<T, 1, 1, false>(a, p, sms, pdl, stream, launches, &err);
-            else if (T::kBytes == 4 && k == 2 && r == 1) done = launch_layernorm_k<T, 2, 1, false>(a, p, sms, pdl, stream, launches, &err);
-            else if (k == 2) done = launch_layernorm_k<T, 2, 2, false>(a, p, sms, pdl, stream, launches, &err);
-            else done = launch_layernorm_k<T, 4, 1, false>(a, p, sms, pdl, stream, launches, &err);
+            if (k == 1) {
+                done = launch_layernorm_k<T, 1, 1, false>(a, p, sms, pdl, stream, launches, &err);
+            } else if (k == 4) {
+                done = launch_layernorm_k<T, 4, 1, false>(a, p, sms, pdl, stream, launches, &err);
+            } else if constexpr (T::kBytes == 2) {
+                done = launch_layernorm_k<T, 2, 2, false>(a, p, sms, pdl, stream, launches, &err);
+            } else if (r == 1) {
+                done = launch_layernorm_k<T, 2, 1, false>(a, p, sms, pdl, stream, launches, &err);
+            } else {      // (two rows at a time: without an add)
+                done = p.edge ? launch_layernorm_tile<T, 2, 2, true, false, false>(a, p, sms, pdl, stream, launches, &err)
+                              : launch_layernorm_tile<T, 2, 2, false, false, false>(a, p, sms, pdl, stream, launches, &err);
+            }
         }
         if (done) return err;
     }

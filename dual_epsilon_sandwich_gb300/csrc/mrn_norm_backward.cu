@@ -461,15 +461,25 @@ cudaError_t launch_backward_typed(const BackwardArgs &a, int sms, bool pdl, cuda
     bool done = false;
     // (a generator group is a slot only when the operands start on a slot boundary)
     if (mis == 0 || (mis > 0 && a.drop.threshold == 0)) {
-        // Slots per thread for rows of a CTA, and threads of one at most.  Measured on GB300, a
-        // 400 MB call each (us): bf16 n = 4096 2 68.3, 3 68.9; 6656 2 68.3, 4 68.8; 16384 in
-        // clusters of CTAs of 64 threads 4 111, of 128 4 118 and 2 122, of 256 4 131.  f32 n = 4096 3 66.8, 1 69.1; 8192 3 67.6; rmsnorm 4096 x 16384
-        // in clusters 2 (of at most 256 threads) 178, 4 182.
+        // Slots per thread (k) for rows of a CTA, and threads of one at most.  Measured on GB300, a
+        // call of 400 to 670 MB (us), with dropout where not said otherwise:
+        //   bf16  n = 4096 2 121.0, 3 125.2, 4 125.5;  4095 2 145.5, 4 151.7;  6656 4 133.7, 2
+        //         137.4;  6655 4 149.5, 2 163.9;  8192 4 129.0, 2 131.2;  without dropout 8191
+        //         2 96.4, 4 99.3;  16384 in clusters of CTAs of 64 threads 4 111, of 128 118
+        //   f32   n = 4096 3 84.2, 2 93.7, 4 94.4;  4095 4 95.3, 2 99.3, 3 113.0;  6656 4 94.9, 3
+        //         100.9;  6655 4 99.3, 2 106.8, 3 112.3;  8191 4 101.1, 3 121.4;  rmsnorm 16384 in
+        //         clusters 2 (of at most 256 threads) 178, 4 182
         const int64_t slots = a.n / 8;
-        int k = T::kBytes == 2 ? (slots <= 1024 ? 2 : 4) : (slots <= 1152 ? 3 : 2);
+        int k;
+        if (T::kBytes == 2) {
+            k = slots > 1024 || (a.dres && slots > 640) ? 4 : 2;
+        } else {
+            const bool edge = mis != 0 || a.n % 8 != 0;
+            k = slots > 1024 ? 2 : (edge || slots > 512 ? 4 : 3);
+        }
         int most_threads = backward_resident(k);
         if (T::kBytes == 4 && k == 2 && slots <= 8192) most_threads = 256;
-        if (T::kBytes == 2 && k == 4) most_threads = slots <= 2048 ? 64 : (slots <= 4096 ? 128 : 256);
+        if (T::kBytes == 2 && slots > 1024) most_threads = slots <= 2048 ? 64 : (slots <= 4096 ? 128 : 256);
         const bool few = tile_few_rows(a.rows, a.n, sms);
         if (few) {
             k = 1;
@@ -482,10 +492,14 @@ cudaError_t launch_backward_typed(const BackwardArgs &a, int sms, bool pdl, cuda
                    : p.k == 3 ? launch_backward_k<T, 3, true>(a, p, l)
                               : launch_backward_k<T, 4, true>(a, p, l);
         } else if (p.ok) {
-            constexpr int kOther = T::kBytes == 2 ? 4 : 3;
-            done = k == 1   ? launch_backward_k<T, 1, false>(a, p, l)
-                   : k == 2 ? launch_backward_k<T, 2, false>(a, p, l)
-                            : launch_backward_k<T, kOther, false>(a, p, l);
+            if constexpr (T::kBytes == 4) {
+                if (k == 3)      // (aligned rows only)
+                    done = a.rms ? launch_backward_tile<T, 3, false, false, true>(a, p, l)
+                                 : launch_backward_tile<T, 3, false, false, false>(a, p, l);
+            }
+            if (k == 1) done = launch_backward_k<T, 1, false>(a, p, l);
+            else if (k == 2) done = launch_backward_k<T, 2, false>(a, p, l);
+            else if (k == 4) done = launch_backward_k<T, 4, false>(a, p, l);
         }
         join.mis = mis;
         join.shifted = done && p.edge && !p.warp;
