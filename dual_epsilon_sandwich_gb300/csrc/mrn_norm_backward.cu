@@ -467,19 +467,20 @@ cudaError_t launch_backward_typed(const BackwardArgs &a, int sms, bool pdl, cuda
         //         137.4;  6655 4 149.5, 2 163.9;  8192 4 129.0, 2 131.2;  without dropout 8191
         //         2 96.4, 4 99.3;  16384 in clusters of CTAs of 64 threads 4 111, of 128 118
         //   f32   n = 4096 3 84.2, 2 93.7, 4 94.4;  4095 4 95.3, 2 99.3, 3 113.0;  6656 4 94.9, 3
-        //         100.9;  6655 4 99.3, 2 106.8, 3 112.3;  8191 4 101.1, 3 121.4;  rmsnorm 16384 in
-        //         clusters 2 (of at most 256 threads) 178, 4 182
+        //         100.9;  6655 4 99.3, 2 106.8, 3 112.3;  8191 4 101.1, 3 121.4;  16384 in
+        //         clusters of CTAs of 256 threads 4 218, 2 224, of 64 4 221;  16383 of 64 4
+        //         230, of 256 4 250;  without dropout 32768 of 128 4 103, of 256 2 107
         const int64_t slots = a.n / 8;
+        const bool edge = mis != 0 || a.n % 8 != 0;
         int k;
         if (T::kBytes == 2) {
             k = slots > 1024 || (a.dres && slots > 640) ? 4 : 2;
         } else {
-            const bool edge = mis != 0 || a.n % 8 != 0;
-            k = slots > 1024 ? 2 : (edge || slots > 512 ? 4 : 3);
+            k = edge || slots > 512 ? 4 : 3;
         }
         int most_threads = backward_resident(k);
-        if (T::kBytes == 4 && k == 2 && slots <= 8192) most_threads = 256;
-        if (T::kBytes == 2 && slots > 1024) most_threads = slots <= 2048 ? 64 : (slots <= 4096 ? 128 : 256);
+        if (slots > 1024 && (T::kBytes == 2 || edge || slots > 2048))
+            most_threads = slots <= 2048 ? 64 : (slots <= (T::kBytes == 2 ? 4096 : 8192) ? 128 : 256);
         const bool few = tile_few_rows(a.rows, a.n, sms);
         if (few) {
             k = 1;
@@ -492,14 +493,16 @@ cudaError_t launch_backward_typed(const BackwardArgs &a, int sms, bool pdl, cuda
                    : p.k == 3 ? launch_backward_k<T, 3, true>(a, p, l)
                               : launch_backward_k<T, 4, true>(a, p, l);
         } else if (p.ok) {
-            if constexpr (T::kBytes == 4) {
-                if (k == 3)      // (aligned rows only)
-                    done = a.rms ? launch_backward_tile<T, 3, false, false, true>(a, p, l)
-                                 : launch_backward_tile<T, 3, false, false, false>(a, p, l);
+            if (k == 1) {
+                done = launch_backward_k<T, 1, false>(a, p, l);
+            } else if (k == 4) {
+                done = launch_backward_k<T, 4, false>(a, p, l);
+            } else if constexpr (T::kBytes == 2) {
+                done = launch_backward_k<T, 2, false>(a, p, l);
+            } else {             // (three: aligned rows)
+                done = a.rms ? launch_backward_tile<T, 3, false, false, true>(a, p, l)
+                             : launch_backward_tile<T, 3, false, false, false>(a, p, l);
             }
-            if (k == 1) done = launch_backward_k<T, 1, false>(a, p, l);
-            else if (k == 2) done = launch_backward_k<T, 2, false>(a, p, l);
-            else if (k == 4) done = launch_backward_k<T, 4, false>(a, p, l);
         }
         join.mis = mis;
         join.shifted = done && p.edge && !p.warp;
