@@ -35,7 +35,9 @@ int64_t backward_parts(int64_t rows, int64_t n, int sms) {
 
 // Any width: one row per CTA at a time, two passes over it (the second out of
 // L2), element by element; the partial sums live in the workspace, each
-// element of them read and written by one thread only.
+// element of them read and written by one thread only.  For the calls that the tile kernel
+// does not take, as in the forward; 16384 x 4096 bf16, x an element off the others, 296 us
+// (the tile kernel: 76).
 template <class T, bool RMS>
 __global__ void __launch_bounds__(kLoopedThreads)
 mrn_norm_backward_looped_kernel(const BackwardArgs a, float *part_gamma, float *part_beta,
@@ -95,7 +97,17 @@ mrn_norm_backward_looped_kernel(const BackwardArgs a, float *part_gamma, float *
 }
 
 // Rows held in registers between their copy and their outputs, the column sums in
-// registers over all rows of the CTA (see mrn_row_tile.cuh).
+// registers over all rows of the CTA (see mrn_row_tile.cuh).  Each operand is read once, and
+// both sums of a row are taken together, so a row costs one barrier.  Measured on GB300, with
+// the join: 16384 x 4096 bf16 76 us (5.3 TB/s, 78 % of the copy's rate), with dropout and a
+// stream's gradient 121 us (5.6 TB/s); 16384 x 4095 bf16 with both 144 us (4.7 TB/s); 4096 x
+// 6656 f32 with both 94 us (5.8 TB/s); RMSNorm 163840 x 128 bf16 24 us (5.2 TB/s), 4096 x 16384
+// f32 in clusters 184 us (5.8 TB/s).
+//   What bounds it: the instructions of the 16 warps that the registers of the column sums leave
+// room for (issued in 53 % of cycles under ncu, dram 57 to 65 % busy; waits for shared memory
+// and for results of arithmetic come first), then the join with its launch, 4 to 6 us.  Where
+// rows start off a slot boundary, the warp that holds their ends lets the others wait (barriers
+// are then the first stall) and half of the rows' sectors are written in two parts.
 template <class T, int K, bool EDGE, bool WARP, bool RMS>
 __global__ void __launch_bounds__(backward_resident(K))
 mrn_norm_backward_tile_kernel(const BackwardArgs a, const TileArgs t, float *part_gamma,
@@ -368,7 +380,9 @@ bool launch_backward_k(const BackwardArgs &a, const TileShape &p, BackwardLaunch
 
 // dgamma (blockIdx.y == 0) and dbeta (1): the sum of `parts` partial rows.  A CTA owns
 // 32 * C columns; its warps take every nth partial row each, all their loads in flight at
-// once where there are few enough, and are joined in shared memory, in order.  shifted: column
+// once where there are few enough, and are joined in shared memory, in order: one trip to L2,
+// which bounds it.  304 rows of 4096 columns, two sums (10 MB): 6.7 us alone out of DRAM under
+// ncu, about 4 behind its backward, whose last rows are still in L2.  shifted: column
 // j of partial row p stands where the tile kernel left it, at j + 8 - (the elements from row
 // p's start to the next slot boundary).
 struct JoinArgs {

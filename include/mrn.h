@@ -240,9 +240,21 @@ mrn_status mrn_seam_scale(const void *u, const void *gamma, void *y, int64_t row
  * LayerNorm and RMSNorm.  Not on the pages, which only run a model.  The
  * conventions above hold (pointers, layout, dtype, alignment, aliasing, stream,
  * errors); rows == 0 is a no-op except where a gradient of weights is due,
- * which is then zero.  Rows need no alignment beyond the element's, but rows
- * whose operands all sit at one offset within 16 bytes are moved in 16-byte
- * granules as described above.
+ * which is then zero.
+ *
+ * Speed and alignment: operands whose base pointers share one offset from a multiple
+ * of eight elements (16 bytes of bf16, 32 of f32), zero as a rule, are moved in whole
+ * slots of eight elements, whatever the row pitch; up to seven elements at either end
+ * of a row whose pitch is not a multiple of eight go one by one (bf16: the four bytes
+ * that hold the element are read, which may take in one element beside the row, never
+ * more).  Operands at different offsets, rows wider than a cluster of CTAs holds (over
+ * 131,072 elements) and, with a dropout, operands off a multiple of eight go element by
+ * element: several times slower, with the same meaning.
+ * Launches: one kernel per call, two for a gradient with weights (the rows, then the
+ * sum of what the CTAs left of dgamma and dbeta); mrn_force_geometry does not apply.
+ * Rows that are split over a cluster wait for each other for about a second at most;
+ * if one runs out, mrn_wait_timeouts() counts it, and the call's remaining rows and its
+ * gradients of weights are unspecified.
  *
  * Dropout and its generator
  *   Element e = r*n + j of the flattened matrix is kept when u16(e) >= t, with
@@ -471,10 +483,11 @@ uint64_t mrn_launch_count(void);
  *                   test hook, never for use: the first wait of every CTA
  *                   of the staged kernels (MRN_GEOM_TMA, staged
  *                   MRN_GEOM_Q8_BLOCKS: its gamma copy) and of cluster
- *                   reductions in MRN_GEOM_CTA (its first message exchange)
- *                   expects 16 bytes more than ever arrive, so it runs out
+ *                   reductions in MRN_GEOM_CTA and the training operations (its
+ *                   first message exchange) expects 16 bytes more than ever arrive, so it runs out
  *                   after about one second.  The staged kernels then write
- *                   nothing; the register kernel's outputs are unspecified.
+ *                   nothing; the register kernel's outputs and the training
+ *                   operations' are unspecified.
  *                   mrn_wait_timeouts() reports the waits; the context stays
  *                   usable.  Lets a test drive the timeout path with no fault.
  * Unknown bits give MRN_ERR_INVALID_GEOMETRY.  Not on the pages: a launch
