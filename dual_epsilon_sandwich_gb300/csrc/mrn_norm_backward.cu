@@ -483,7 +483,8 @@ cudaError_t launch_backward_typed(const BackwardArgs &a, int sms, bool pdl, cuda
         //   f32   n = 4096 3 84.2, 2 93.7, 4 94.4;  4095 4 95.3, 2 99.3, 3 113.0;  6656 4 94.9, 3
         //         100.9;  6655 4 99.3, 2 106.8, 3 112.3;  8191 4 101.1, 3 121.4;  16384 in
         //         clusters of CTAs of 256 threads 4 218, 2 224, of 64 4 221;  16383 of 64 4
-        //         230, of 256 4 250;  without dropout 32768 of 128 4 103, of 256 2 107
+        //         230, of 256 4 250;  rmsnorm 12288 4 133, 2 of 512 137;  16384 4 183, 2 of 512
+        //         175;  24576 4 136, 2 of 512 148
         const int64_t slots = a.n / 8;
         const bool edge = mis != 0 || a.n % 8 != 0;
         int k;

@@ -14,7 +14,7 @@ namespace mrn {
 // with the key advanced by the Weyl constants between rounds.  The counter of
 // element e is (e / 8, offset + site), 64 bits each, and the key is the seed;
 // the 128 bits of the result are eight lanes of 16, so that one evaluation
-// serves eight elements: a probability on a grid of 2^-16 costs a quarter of
+// serves eight elements: a probability on a grid of 2^-16 costs half of
 // what 32 bits per element would.  Nothing is stored: the gradient evaluates
 // the same counters again.
 // ---------------------------------------------------------------------------
@@ -145,9 +145,8 @@ __device__ __forceinline__ void cta_sum(float (&v)[1], CtaSumSlots<1> &s, int &t
     v[0] = warp_allsum(lane < nwarps ? s.v[p][0][lane] : 0.0f);
 }
 
-// Two and four values at once (at most 16 warps): the first exchanges leave one value with
-// each half or quarter of the warp, so that all of them take little more than the shuffles
-// of one.
+// Two values at once (at most 16 warps): the first exchange leaves one value with each half of
+// the warp, so that both take little more than the shuffles of one.
 __device__ __forceinline__ void cta_sum(float (&v)[2], CtaSumSlots<2> &s, int &turn) {
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;
@@ -164,29 +163,6 @@ __device__ __forceinline__ void cta_sum(float (&v)[2], CtaSumSlots<2> &s, int &t
     for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
     v[0] = __shfl_sync(0xFFFFFFFFu, t, 0);
     v[1] = __shfl_sync(0xFFFFFFFFu, t, 16);
-}
-
-__device__ __forceinline__ void cta_sum(float (&v)[4], CtaSumSlots<4> &s, int &turn) {
-    const int lane = threadIdx.x & 31;
-    const int warp = threadIdx.x >> 5;
-    const int nwarps = blockDim.x >> 5;
-    const int quarter = lane >> 3, upper = lane >> 4, odd = quarter & 1;
-    const int p = ++turn & 1;
-    // the upper half of the warp keeps values 2 and 3, the lower 0 and 1
-    const float a = (upper ? v[2] : v[0]) + __shfl_xor_sync(0xFFFFFFFFu, upper ? v[0] : v[2], 16);
-    const float b = (upper ? v[3] : v[1]) + __shfl_xor_sync(0xFFFFFFFFu, upper ? v[1] : v[3], 16);
-    float t = (odd ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, odd ? a : b, 8);
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
-    if ((lane & 7) == 0) s.v[p][quarter][warp] = t;
-    __syncthreads();
-    const int w = lane & 7;
-    t = (w < nwarps ? s.v[p][quarter][w] : 0.0f) +
-        (w + 8 < nwarps ? s.v[p][quarter][w + 8] : 0.0f);
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, t, 8 * i);
 }
 
 // One kernel launch with the library's programmatic dependent launch option.
@@ -251,25 +227,6 @@ template <class T> struct Slot {
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
-        }
-    }
-    __device__ __forceinline__ void clear(int i) {
-        if constexpr (T::kBytes == 4) {
-            w[i] = 0u;
-        } else {
-            w[i >> 1] &= (i & 1) ? 0x0000FFFFu : 0xFFFF0000u;
-        }
-    }
-    // element i alone at p, when `on` is not 0 (a predicated store, no branch)
-    __device__ __forceinline__ void st_one_if(char *p, int i, uint32_t on) const {
-        if constexpr (T::kBytes == 4) {
-            asm volatile("{.reg .pred q; setp.ne.u32 q, %2, 0; @q st.global.u32 [%0], %1;}"
-                         :: "l"(p), "r"(w[i]), "r"(on) : "memory");
-        } else {
-            const unsigned short h =
-                static_cast<unsigned short>((i & 1) ? (w[i >> 1] >> 16) : (w[i >> 1] & 0xFFFFu));
-            asm volatile("{.reg .pred q; setp.ne.u32 q, %2, 0; @q st.global.u16 [%0], %1;}"
-                         :: "l"(p), "h"(h), "r"(on) : "memory");
         }
     }
 };
