@@ -24,10 +24,11 @@ template <class T> constexpr int forward_threads(int k, int r) {
 // Any width: one row per CTA at a time, three passes over it (the second and
 // third out of L2), element by element.  For operands that do not share an offset and rows
 // wider than a cluster holds.  Bound by its accesses of one element: 16384 x 4096 bf16, x an
-// element off the others, 312 us alone and 539 after the add (the tile kernel: 45 and 90).
+// element off the others, 312 us alone and 539 after the add (the tile kernel: 45 and 89).
 template <class T>
 __global__ void __launch_bounds__(kLoopedThreads) mrn_layernorm_looped_kernel(const LayernormArgs a) {
-    __shared__ CtaSumSlots<1> slots;
+    __shared__ CtaSum slots;
+    cta_sum_setup(slots);
     pdl_enter();
     int turn = 0;
     const DropKey key = drop_key(a.drop);
@@ -69,9 +70,9 @@ __global__ void __launch_bounds__(kLoopedThreads) mrn_layernorm_looped_kernel(co
 
 // Rows held in registers between their copy and their outputs (see mrn_row_tile.cuh): the
 // deviations are taken from the values themselves, so that every operand is read once and every
-// output written once.  Measured on GB300: 16384 x 4096 bf16 45.2 us alone (5.9 TB/s, 88 % of
-// the copy's rate) and 90.5 after the add (5.9 TB/s); 4096 x 6655 f32 after the add 77.9 us
-// (5.6 TB/s); 4 x 6656 f32 2.6 us, a launch and two sums over a cluster.
+// output written once.  Measured on GB300: 16384 x 4096 bf16 44.5 us alone (6.0 TB/s, 89 % of
+// the copy's rate) and 88.7 after the add (6.1 TB/s); 4096 x 6655 f32 after the add 76.1 us
+// (5.7 TB/s); 4 x 6656 f32 2.5 us, a launch and two sums over a cluster.
 //   What bounds it: not memory alone (dram 68 % busy under ncu) but the instructions of 16 warps
 // on an SM, issued in 56 % of cycles, with the generator's and the conversions' the most of
 // them; a row's two sums, each a barrier of its CTA, are covered by the copies in flight and
@@ -80,7 +81,7 @@ template <class T, int K, int R, bool EDGE, bool WARP, bool ADD>
 __global__ void __launch_bounds__(forward_resident<T>(K, R))
 mrn_layernorm_tile_kernel(const LayernormArgs a, const TileArgs t) {
     extern __shared__ __align__(16) unsigned char ring_bytes[];
-    __shared__ RowSumSlots<R> slots;
+    __shared__ RowSumSlots<R, T::kBytes == 2> slots;
     constexpr int kOps = ADD ? 2 : 1;
     __shared__ EndSlots<kOps, R, EDGE, WARP> end_w;
     RowTile<T, K, R, EDGE, WARP> tile(a.rows, a.n, t);
@@ -157,7 +158,7 @@ mrn_layernorm_tile_kernel(const LayernormArgs a, const TileArgs t) {
                 sum[rr] += end[rr];
             }
         }
-        if (!row_sum<R, WARP>(sum, slots, turn, tile.width, tile.cl, tile.crank, turn == 0 ? t.stall : 0u)) break;
+        if (!row_sum<WARP>(sum, slots, turn, tile.width, tile.cl, tile.crank, turn == 0 ? t.stall : 0u)) break;
         float dev[R];
 #pragma unroll
         for (int rr = 0; rr < R; ++rr) {
@@ -177,7 +178,7 @@ mrn_layernorm_tile_kernel(const LayernormArgs a, const TileArgs t) {
             dev[rr] = f2_sum(acc);
             if (EDGE && tile.end_col >= 0) dev[rr] = fmaf(end[rr] - sum[rr], end[rr] - sum[rr], dev[rr]);
         }
-        if (!row_sum<R, WARP>(dev, slots, turn, tile.width, tile.cl, tile.crank, 0u)) break;
+        if (!row_sum<WARP>(dev, slots, turn, tile.width, tile.cl, tile.crank, 0u)) break;
         uint64_t minus[R], scale[R];
 #pragma unroll
         for (int rr = 0; rr < R; ++rr) {

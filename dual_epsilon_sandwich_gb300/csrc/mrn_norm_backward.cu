@@ -42,7 +42,7 @@ template <class T, bool RMS>
 __global__ void __launch_bounds__(kLoopedThreads)
 mrn_norm_backward_looped_kernel(const BackwardArgs a, float *part_gamma, float *part_beta,
                                 const int64_t part_stride) {
-    __shared__ CtaSumSlots<2> slots;
+    __shared__ CtaSumHalves slots;
     pdl_enter();
     int turn = 0;
     const DropKey key = drop_key(a.drop);
@@ -100,9 +100,9 @@ mrn_norm_backward_looped_kernel(const BackwardArgs a, float *part_gamma, float *
 // registers over all rows of the CTA (see mrn_row_tile.cuh).  Each operand is read once, and
 // both sums of a row are taken together, so a row costs one barrier.  Measured on GB300, with
 // the join: 16384 x 4096 bf16 76 us (5.3 TB/s, 78 % of the copy's rate), with dropout and a
-// stream's gradient 121 us (5.6 TB/s); 16384 x 4095 bf16 with both 144 us (4.7 TB/s); 4096 x
-// 6656 f32 with both 94 us (5.8 TB/s); RMSNorm 163840 x 128 bf16 24 us (5.2 TB/s), 4096 x 16384
-// f32 in clusters 184 us (5.8 TB/s).
+// stream's gradient 121 us (5.6 TB/s); 16384 x 4095 bf16 with both 138 us (4.9 TB/s); 4096 x
+// 6656 f32 with both 92 us (5.9 TB/s); RMSNorm 163840 x 128 bf16 24 us (5.2 TB/s), 4096 x 16384
+// f32 in clusters 178 us (6.0 TB/s).
 //   What bounds it: the instructions of the 16 warps that the registers of the column sums leave
 // room for (issued in 53 % of cycles under ncu, dram 57 to 65 % busy; waits for shared memory
 // and for results of arithmetic come first), then the join with its launch, 4 to 6 us.  Where
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(backward_resident(K))
 mrn_norm_backward_tile_kernel(const BackwardArgs a, const TileArgs t, float *part_gamma,
                               float *part_beta, const int64_t part_stride) {
     extern __shared__ __align__(16) unsigned char ring_bytes[];
-    __shared__ RowSumSlots<2> slots;
+    __shared__ RowSumSlots<2, T::kBytes == 2 && !RMS> slots;
     __shared__ float stats[kTileMaxStages][2][kWarpTileThreads];   // mean and rstd, per team
     __shared__ EndSlots<3, 1, EDGE, WARP> end_w;
     RowTile<T, K, 1, EDGE, WARP> tile(a.rows, a.n, t);
@@ -211,7 +211,7 @@ mrn_norm_backward_tile_kernel(const BackwardArgs a, const TileArgs t, float *par
             }
             s[1] = fmaf(ew, end_xh, s[1]);
         }
-        if (!row_sum<2, WARP>(s, slots, turn, tile.width, tile.cl, tile.crank, turn == 0 ? t.stall : 0u)) break;
+        if (!row_sum<WARP>(s, slots, turn, tile.width, tile.cl, tile.crank, turn == 0 ? t.stall : 0u)) break;
         // ds = rstd w - rstd c1 - xh rstd c2
         float c1 = 0.0f, c2;
         if (RMS) {

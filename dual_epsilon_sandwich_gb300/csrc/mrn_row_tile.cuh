@@ -78,14 +78,15 @@ __device__ __forceinline__ void ld_shared_slot(Slot<F32> &s, uint32_t p) {
 // stores of the row before it (16384 f32: 193 us against 178 for the gradient of
 // 4096 rows).  Boxes and mbarriers alternate: a CTA sends turn t + 2 only after it has every
 // peer's t + 1, which a peer sends only after all its threads have read t.
-template <int N> struct RowSumSlots {
-    CtaSumSlots<N> cta;
+template <int N, bool PAIRS> struct RowSumSlots {
+    typename CtaSumOf<N, PAIRS>::Slots cta;
     float box[2][N][kMaxCluster];   // [turn parity][value][sender rank]
     __align__(8) uint64_t bar[2];
 };
 
-// Before the first row_sum of a cluster, by every thread: every peer's mbarriers are set up.
-template <int N> __device__ __forceinline__ void row_sum_setup(RowSumSlots<N> &s, unsigned cl) {
+// Before the first row_sum, by every thread: the slots and every peer's mbarriers are set up.
+template <int N, bool PAIRS> __device__ __forceinline__ void row_sum_setup(RowSumSlots<N, PAIRS> &s, unsigned cl) {
+    cta_sum_setup(s.cta);
     if (cl > 1) {
         if (threadIdx.x == 0) {
             mbar_init(&s.bar[0], 1);
@@ -110,8 +111,8 @@ __device__ __forceinline__ void row_sum_leave(unsigned cl) {
 // False (in the whole CTA) when a peer's message did not arrive in time (about a second): the
 // CTA then stops, and its peers after it.  `stall`: bytes more than ever arrive that a wait
 // expects (a test hook, 0 in use).
-template <int N, bool WARP>
-__device__ __forceinline__ bool row_sum(float (&v)[N], RowSumSlots<N> &s, int &turn, int width,
+template <bool WARP, int N, bool PAIRS>
+__device__ __forceinline__ bool row_sum(float (&v)[N], RowSumSlots<N, PAIRS> &s, int &turn, int width,
                                         unsigned cl, unsigned crank, uint32_t stall) {
     if constexpr (WARP) {
 #pragma unroll

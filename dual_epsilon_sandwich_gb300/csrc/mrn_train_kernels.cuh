@@ -125,29 +125,53 @@ __device__ __forceinline__ float drop_add(float v, float r, bool keep, float sca
     return keep ? fmaf(v, scale, r) : r;
 }
 
-// ---------------------------------------------------------------------------
-// Sums over all threads of a CTA (a multiple of 32), one barrier each: the
-// slots alternate between calls, so that a call's writes never meet the reads
-// of the call before it.
-// ---------------------------------------------------------------------------
-template <int N> struct CtaSumSlots {
-    float v[2][N][32];
-};
-
-__device__ __forceinline__ void cta_sum(float (&v)[1], CtaSumSlots<1> &s, int &turn) {
-    const int lane = threadIdx.x & 31;
-    const int warp = threadIdx.x >> 5;
-    const int nwarps = blockDim.x >> 5;
-    const int p = ++turn & 1;
-    v[0] = warp_allsum(v[0]);
-    if (lane == 0) s.v[p][0][warp] = v[0];
-    __syncthreads();
-    v[0] = warp_allsum(lane < nwarps ? s.v[p][0][lane] : 0.0f);
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float f2_sum(uint64_t v) {
+    float lo, hi;
+    f2_unpack(v, lo, hi);
+    return lo + hi;
 }
 
-// Two values at once (at most 16 warps): the first exchange leaves one value with each half of
-// the warp, so that both take little more than the shuffles of one.
-__device__ __forceinline__ void cta_sum(float (&v)[2], CtaSumSlots<2> &s, int &turn) {
+// ---------------------------------------------------------------------------
+// Sums over all threads of a CTA (a multiple of 32, at most 512), one barrier each: the
+// slots alternate between calls, so that a call's writes never meet the reads
+// of the call before it.  What stands behind the barrier is on every row's path: the fewer
+// shuffles, the better.  cta_sum_setup, before the first sum, zeroes the slots of warps that
+// the CTA does not have.
+// ---------------------------------------------------------------------------
+constexpr int kCtaWarps = 16;
+
+// One value.
+struct CtaSum {
+    __align__(16) float v[2][kCtaWarps];
+};
+__device__ __forceinline__ void cta_sum_setup(CtaSum &s) {
+    const int warp = static_cast<int>(blockDim.x >> 5) + static_cast<int>(threadIdx.x);
+    if (warp < kCtaWarps) s.v[0][warp] = s.v[1][warp] = 0.0f;
+}
+__device__ __forceinline__ void cta_sum(float (&v)[1], CtaSum &s, int &turn) {
+    const int lane = threadIdx.x & 31;
+    const int p = ++turn & 1;
+    v[0] = warp_allsum(v[0]);
+    if (lane == 0) s.v[p][threadIdx.x >> 5] = v[0];
+    __syncthreads();
+    float t = s.v[p][lane & 7] + s.v[p][(lane & 7) + 8];
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+    v[0] = t;
+}
+
+// Two values: the first exchange leaves one value with each half of the warp, so that both take
+// little more than the shuffles of one.  Joined by shuffles: the fewest registers (f32, RMSNorm).
+struct CtaSumHalves {
+    float v[2][2][32];
+};
+__device__ __forceinline__ void cta_sum_setup(CtaSumHalves &) {}
+__device__ __forceinline__ void cta_sum(float (&v)[2], CtaSumHalves &s, int &turn) {
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;
     const int nwarps = blockDim.x >> 5;
@@ -164,6 +188,43 @@ __device__ __forceinline__ void cta_sum(float (&v)[2], CtaSumSlots<2> &s, int &t
     v[0] = __shfl_sync(0xFFFFFFFFu, t, 0);
     v[1] = __shfl_sync(0xFFFFFFFFu, t, 16);
 }
+
+// Two values, a warp's side by side: every thread reads all the pairs, four warps in two loads,
+// and adds them in order: one trip to shared memory in place of six shuffles, and more
+// registers.  Measured on GB300, us a call, against halves: bf16 LayerNorm gradient 16384 x
+// 4095 85.8 (90.5), the tail's 138 (144), the tail 16384 x 4096 88.8 (90.3), but RMSNorm's
+// gradient 16384 x 4096, whose rows are read again behind the sums, 78.3 (72.9), and in f32 the
+// tail's gradient 4096 x 6656, at the register limit, 100 (95).
+struct CtaSumPairs {
+    __align__(16) float v[2][kCtaWarps][2];
+};
+__device__ __forceinline__ void cta_sum_setup(CtaSumPairs &s) {
+    const int warp = static_cast<int>(blockDim.x >> 5) + static_cast<int>(threadIdx.x);
+    if (warp < kCtaWarps) s.v[0][warp][0] = s.v[0][warp][1] = s.v[1][warp][0] = s.v[1][warp][1] = 0.0f;
+}
+__device__ __forceinline__ void cta_sum(float (&v)[2], CtaSumPairs &s, int &turn) {
+    const int lane = threadIdx.x & 31;
+    const int half = lane >> 4;
+    const int p = ++turn & 1;
+    float t = (half ? v[1] : v[0]) + __shfl_xor_sync(0xFFFFFFFFu, half ? v[0] : v[1], 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+    if ((lane & 15) == 0) s.v[p][threadIdx.x >> 5][half] = t;
+    __syncthreads();
+    const ulonglong2 *w = reinterpret_cast<const ulonglong2 *>(s.v[p]);
+    const auto four = [&](int i) {
+        const ulonglong2 a = w[i], b = w[i + 1];
+        return f2_add(f2_add(a.x, a.y), f2_add(b.x, b.y));
+    };
+    uint64_t both = f2_add(four(0), four(2));
+    if (blockDim.x > 256) both = f2_add(both, f2_add(four(4), four(6)));
+    f2_unpack(both, v[0], v[1]);
+}
+
+// The form for N values.
+template <int N, bool PAIRS> struct CtaSumOf { using Slots = CtaSum; };
+template <> struct CtaSumOf<2, true> { using Slots = CtaSumPairs; };
+template <> struct CtaSumOf<2, false> { using Slots = CtaSumHalves; };
 
 // One kernel launch with the library's programmatic dependent launch option.
 template <class... Params, class... Args>
@@ -230,17 +291,6 @@ template <class T> struct Slot {
         }
     }
 };
-
-__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ float f2_sum(uint64_t v) {
-    float lo, hi;
-    f2_unpack(v, lo, hi);
-    return lo + hi;
-}
 
 // A whole slot, aligned to its size; read once (past L1).
 __device__ __forceinline__ void ld_slot(Slot<BF16> &s, const void *p) {
