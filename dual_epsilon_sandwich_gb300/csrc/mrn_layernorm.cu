@@ -73,8 +73,8 @@ __global__ void __launch_bounds__(kLoopedThreads) mrn_layernorm_looped_kernel(co
 // output written once.  Measured on GB300: 16384 x 4096 bf16 44.5 us alone (6.0 TB/s, 89 % of
 // the copy's rate) and 88.7 after the add (6.1 TB/s); 4096 x 6655 f32 after the add 76.1 us
 // (5.7 TB/s); 4 x 6656 f32 2.5 us, a launch and two sums over a cluster.
-//   What bounds it: not memory alone (dram 68 % busy under ncu) but the instructions of 16 warps
-// on an SM, issued in 56 % of cycles, with the generator's and the conversions' the most of
+//   What bounds it: not memory alone (dram 69 % busy under ncu) but the instructions of 16 warps
+// on an SM, issued in 55 % of cycles, with the generator's and the conversions' the most of
 // them; a row's two sums, each a barrier of its CTA, are covered by the copies in flight and
 // by the other CTA of the SM.  More warps would need fewer registers than a row's slots take.
 template <class T, int K, int R, bool EDGE, bool WARP, bool ADD>

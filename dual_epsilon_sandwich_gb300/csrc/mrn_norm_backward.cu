@@ -104,7 +104,7 @@ mrn_norm_backward_looped_kernel(const BackwardArgs a, float *part_gamma, float *
 // 6656 f32 with both 92 us (5.9 TB/s); RMSNorm 163840 x 128 bf16 24 us (5.2 TB/s), 4096 x 16384
 // f32 in clusters 178 us (6.0 TB/s).
 //   What bounds it: the instructions of the 16 warps that the registers of the column sums leave
-// room for (issued in 53 % of cycles under ncu, dram 57 to 65 % busy; waits for shared memory
+// room for (issued in 54 % of cycles under ncu, dram 60 to 65 % busy; waits for shared memory
 // and for results of arithmetic come first), then the join with its launch, 4 to 6 us.  Where
 // rows start off a slot boundary, the warp that holds their ends lets the others wait (barriers
 // are then the first stall) and half of the rows' sectors are written in two parts.
