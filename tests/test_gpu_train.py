@@ -1,5 +1,9 @@
 """The training operations on the GPU against their 64-bit reference: LayerNorm, the
 residual add with dropout, and the gradients of LayerNorm and RMSNorm."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -9,6 +13,7 @@ from dual_epsilon_sandwich_gb300 import mrn
 
 pytestmark = pytest.mark.gpu
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
 DTYPES = ("f32", "bf16")
 SEED, OFFSET, SITE = -0x123456789ABCDEF, 0x7FFFFFFFFFFFFFF0, 21   # the step's low half wraps
@@ -733,3 +738,40 @@ def test_a_cluster_whose_messages_are_late_stops_and_recovers():
     ref.check(f64(dx), wx, tx, "f32", "dx after a timeout")
     ref.check(f64(dg), wg, tg, "f32", "dgamma after a timeout")
     assert mrn.mrn_wait_timeouts() == 0
+
+
+FIRST_CALLS_CAPTURED = """
+import torch
+from dual_epsilon_sandwich_gb300 import mrn
+x = torch.randn(40, 20001, device="cuda")
+dy, res = torch.randn_like(x), torch.randn_like(x)
+g, b = torch.rand(20001, device="cuda"), torch.rand(20001, device="cuda")
+mean, rstd = torch.empty(40, device="cuda"), torch.empty(40, device="cuda")
+rng = torch.tensor([3, 4], device="cuda")
+stream, normed, dx, dres = (torch.empty_like(x) for _ in range(4))
+dg, db = torch.empty_like(g), torch.empty_like(g)
+ws = mrn.norm_backward_workspace(x)
+
+def step():
+    mrn.dropout_add_layernorm(x, res, g, b, 1e-5, 0.1, rng, out_stream=stream, normed=normed,
+                              mean=mean, rstd=rstd)
+    mrn.dropout_add_layernorm_backward(dy, stream, g, mean, rstd, 0.1, rng, dx=dx, dresidual=dres,
+                                       dgamma=dg, dbeta=db, workspace=ws)
+    return [t.clone() for t in (stream, normed, dx, dres, dg, db)]
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(u, v) for u, v in zip(got, step()))
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_captured():
+    """What the library asks of a kernel at its first call may be asked inside a capture."""
+    out = subprocess.run([sys.executable, "-c", FIRST_CALLS_CAPTURED], cwd=ROOT, timeout=300,
+                         capture_output=True, text=True)
+    assert out.returncode == 0 and out.stdout.strip() == "same", out.stderr[-2000:]
