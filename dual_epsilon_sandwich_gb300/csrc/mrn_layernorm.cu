@@ -3,8 +3,9 @@
 //   stream = res + dropout(x), rounded once to the row type and stored
 //   mean = sum_j s_j / n,  rstd = 1 / sqrt(sum_j (s_j - mean)^2 / n + eps)
 //   y = (s - mean) * rstd * gamma + beta      (s the stored stream, or x)
-// The variance is summed from the deviations, not from the squares: a row
-// whose mean is far from zero loses no digits.
+// The variance is summed from the deviations, not from the squares: what a row whose mean
+// is far from zero loses is the roundings of its f32 mean alone.  Those are the sum's: the
+// quotient by n is rounded once (mean_of below).
 #include "mrn_row_tile.cuh"
 
 namespace mrn {
@@ -19,6 +20,23 @@ template <class T> constexpr int forward_resident(int k, int r) {
 // Threads of a CTA at most.
 template <class T> constexpr int forward_threads(int k, int r) {
     return forward_resident<T>(k, r) < 512 ? forward_resident<T>(k, r) : 512;
+}
+
+// sum / n, rounded to nearest, from the reciprocal inv = 1 / n that is itself rounded to
+// nearest: Markstein's step ("Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990).  q is within one and a half units of the quotient; what the fma leaves of
+// sum is a whole multiple of q's unit, of at most 1.5 n units, and exact; times inv it takes q to
+// within 2^-23 units of the quotient.  A quotient by n <= 2^18 (all that the row tiles hold) lies
+// 2^-19 units at least from the border between two f32 numbers, so that the last addition rounds
+// as the quotient itself would be rounded.
+//   The product alone missed it by up to a unit: a constant row of 1000.0, n = 6656, whose sum is
+// exact, came out 0.02 off beta at eps 1e-5 and 0.5 off at 1e-8.  Every row waits for this; measured
+// on GB300, us with the product, so, and with a division: f32 8192 x 4096 45.8, 46.6, 47.5, bf16
+// 16384 x 4096 after the add 89.6, 90.3, 92.1, f32 64 x 1024 1.83, 1.89, 1.89.
+__device__ __forceinline__ float mean_of(float sum, float n, float inv) {
+    const float q = sum * inv;
+    const float left = fmaf(-q, n, sum);
+    return left == left ? fmaf(left, inv, q) : q;     // (an infinite sum leaves NaN)
 }
 
 // Any width: one row per CTA at a time, three passes over it (the second and
@@ -110,7 +128,7 @@ mrn_layernorm_tile_kernel(const LayernormArgs a, const TileArgs t) {
     const float end_gamma = EDGE ? tile.end_weight(a.gamma) : 0.0f;
     const float end_beta = EDGE && a.beta ? tile.end_weight(a.beta) : 0.0f;
     row_sum_ready(tile.cl);
-    const float inv_n = 1.0f / static_cast<float>(a.n);
+    const float count = static_cast<float>(a.n), inv_n = 1.0f / count;
     int turn = 0;
     for (; tile.cta_left > 0; tile.advance(), walk.next()) {
         __syncwarp();
@@ -162,7 +180,7 @@ mrn_layernorm_tile_kernel(const LayernormArgs a, const TileArgs t) {
         float dev[R];
 #pragma unroll
         for (int rr = 0; rr < R; ++rr) {
-            sum[rr] *= inv_n;     // the mean
+            sum[rr] = mean_of(sum[rr], count, inv_n);
             const uint64_t minus = f2_pack(-sum[rr], -sum[rr]);
             uint64_t acc = 0;
 #pragma unroll
