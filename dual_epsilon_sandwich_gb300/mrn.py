@@ -506,9 +506,20 @@ def seam_scale(u, gamma, out=None):
 # tensors of a call are on one device, which need not be the current one; the
 # work runs on that device's current stream.  (The checks take one test per tensor
 # where nothing is wrong: a call's host time is what a small call costs.)
+#
+# What a helper returns has no autograd history.  So that no gradient is lost in silence, a tensor
+# that requires one is refused while autograd records: the helpers are called under
+# torch.no_grad(), or from the forward and backward of a torch.autograd.Function.
 # ---------------------------------------------------------------------------
+_torch = None     # from the first call on (the mrn_* functions do without torch)
+
+
 def _train_rows(x, name):
     """(rows, n, dtype code, device index) of the tensor that fixes a call's shape."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
     dt = _dtype_code(x)
     dev = x.get_device()
     if dev < 0 or not x.is_contiguous():
@@ -525,11 +536,21 @@ def _fits(t, name, dtype, shape, dev):
     if t.dtype != dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
         _check(t, name, dtype, shape)
         raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    if t.requires_grad:
+        _no_history(t, name)
+
+
+def _no_history(t, name):
+    """Refuses t, which requires a gradient, while autograd records."""
+    if _torch.is_grad_enabled():
+        raise ValueError(f"{name} requires a gradient, which this call would lose: call it under "
+                         "torch.no_grad(), or from a torch.autograd.Function with the gradient "
+                         "as its backward")
 
 
 def _rng_ptr(rng, dev, p):
     """rng: int64 or uint64 tensor {seed, offset} on the device; None when p == 0."""
-    import torch
+    torch = _torch
     if rng is None:
         if p != 0:
             raise ValueError("rng is required when p > 0")
@@ -542,7 +563,7 @@ def _rng_ptr(rng, dev, p):
 
 def _run(what, dev, fn, *args):
     """fn(*args, stream) on device dev and its current stream."""
-    import torch
+    torch = _torch
     if dev == torch._C._cuda_getDevice():
         st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
@@ -554,7 +575,7 @@ def _run(what, dev, fn, *args):
 
 def _stats(mean, rstd, rows, dev):
     """Pointers of the row statistics; both or neither."""
-    import torch
+    torch = _torch
     if mean is None and rstd is None:
         return 0, 0
     if mean is None or rstd is None:
@@ -564,23 +585,23 @@ def _stats(mean, rstd, rows, dev):
                 not t.is_contiguous():
             _check(t, name, torch.float32)
             raise ValueError(f"{name} must hold one value per row ({rows}) on cuda:{dev}")
+        if t.requires_grad:
+            _no_history(t, name)
     return mean.data_ptr(), rstd.data_ptr()
 
 
 def _row_output(t, name, x, dev):
     """t, or a new tensor like x when it is None."""
     if t is None:
-        import torch
-        return torch.empty_like(x)
+        return _torch.empty_like(x)
     _fits(t, name, x.dtype, x.shape, dev)
     return t
 
 
 def _weight_gradient(t, name, n, x, dev):
-    import torch
     if t is None:
-        return torch.empty(n, dtype=torch.float32, device=x.device)
-    _fits(t, name, torch.float32, (n,), dev)
+        return _torch.empty(n, dtype=_torch.float32, device=x.device)
+    _fits(t, name, _torch.float32, (n,), dev)
     return t
 
 
@@ -588,15 +609,14 @@ def norm_backward_workspace(x):
     """Workspace (uint8 tensor) for the gradients of norms over x's last dimension,
     on x's device.  Reusable by later calls of this shape on one stream; calls that
     may run at the same time need one each."""
-    import torch
     rows, n, _, dev = _train_rows(x, "x")
-    with torch.cuda.device(dev):
-        return torch.empty(mrn_norm_backward_workspace(rows, n), dtype=torch.uint8,
-                           device=x.device)
+    with _torch.cuda.device(dev):
+        return _torch.empty(mrn_norm_backward_workspace(rows, n), dtype=_torch.uint8,
+                            device=x.device)
 
 
 def _workspace(workspace, x, dev):
-    import torch
+    torch = _torch
     if workspace is None:
         return norm_backward_workspace(x)
     if workspace.dtype != torch.uint8 or workspace.get_device() != dev or \
@@ -611,6 +631,8 @@ def layernorm(x, gamma, beta, eps: float, out=None, mean=None, rstd=None):
     rstd (float32, one per row), when given, receive the row statistics that
     layernorm_backward takes."""
     rows, n, dt, dev = _train_rows(x, "x")
+    if x.requires_grad:
+        _no_history(x, "x")
     _fits(gamma, "gamma", x.dtype, (n,), dev)
     if beta is not None:
         _fits(beta, "beta", x.dtype, (n,), dev)
@@ -625,6 +647,8 @@ def dropout_add(x, residual, p: float, rng, site: int = 0, out=None):
     """residual + dropout(x); residual None gives dropout(x) alone, which is also the
     gradient's form.  rng: device tensor {seed, offset}; out may be x or residual."""
     rows, n, dt, dev = _train_rows(x, "x")
+    if x.requires_grad:
+        _no_history(x, "x")
     if residual is not None:
         _fits(residual, "residual", x.dtype, x.shape, dev)
     out = _row_output(out, "out", x, dev)
@@ -639,6 +663,8 @@ def dropout_add_layernorm(x, residual, gamma, beta, eps: float, p: float, rng, s
     """(out_stream, normed): out_stream = residual + dropout(x), normed =
     layernorm(out_stream).  out_stream may be x or residual (in place)."""
     rows, n, dt, dev = _train_rows(x, "x")
+    if x.requires_grad:
+        _no_history(x, "x")
     _fits(residual, "residual", x.dtype, x.shape, dev)
     _fits(gamma, "gamma", x.dtype, (n,), dev)
     if beta is not None:
@@ -655,6 +681,8 @@ def dropout_add_layernorm(x, residual, gamma, beta, eps: float, p: float, rng, s
 
 def _backward_operands(dy, x, gamma, dstream, dx, dgamma):
     rows, n, dt, dev = _train_rows(x, "x")
+    if x.requires_grad:
+        _no_history(x, "x")
     _fits(dy, "dy", x.dtype, x.shape, dev)
     _fits(gamma, "gamma", x.dtype, (n,), dev)
     pd = 0
