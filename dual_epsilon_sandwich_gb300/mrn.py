@@ -509,18 +509,26 @@ def seam_scale(u, gamma, out=None):
 #
 # What a helper returns has no autograd history.  So that no gradient is lost in silence, a tensor
 # that requires one is refused while autograd records: the helpers are called under
-# torch.no_grad(), or from the forward and backward of a torch.autograd.Function.
+# torch.no_grad(), or from the forward and backward of a torch.autograd.Function.  What a call
+# writes has its version advanced, so that autograd notices where it had kept the tensor.
 # ---------------------------------------------------------------------------
-_torch = None     # from the first call on (the mrn_* functions do without torch)
+# torch and what every call takes of it, from the first call on (the mrn_* functions do without)
+_torch = _written = _current_device = _raw_stream = None
+
+
+def _load_torch():
+    global _torch, _written, _current_device, _raw_stream
+    import torch
+    _written = torch._C._increment_version     # (of a tuple of tensors)
+    _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    _torch = torch
 
 
 def _train_rows(x, name):
     """(rows, n, dtype code, device index) of the tensor that fixes a call's shape."""
-    global _torch
     if _torch is None:
-        import torch
-        _torch = torch
-    dt = _dtype_code(x)
+        _load_torch()
+    dt = MRN_F32 if x.dtype == _torch.float32 else _dtype_code(x)
     dev = x.get_device()
     if dev < 0 or not x.is_contiguous():
         _check(x, name, x.dtype)
@@ -550,44 +558,46 @@ def _no_history(t, name):
 
 def _rng_ptr(rng, dev, p):
     """rng: int64 or uint64 tensor {seed, offset} on the device; None when p == 0."""
-    torch = _torch
     if rng is None:
         if p != 0:
             raise ValueError("rng is required when p > 0")
         return 0
-    if rng.dtype != torch.int64 and rng.dtype != torch.uint64:
-        raise TypeError(f"rng has dtype {rng.dtype}, expected int64 or uint64")
-    _fits(rng, "rng", rng.dtype, (2,), dev)
+    dtype = rng.dtype
+    if dtype != _torch.int64 and dtype != _torch.uint64:
+        raise TypeError(f"rng has dtype {dtype}, expected int64 or uint64")
+    if rng.get_device() != dev or rng.shape != (2,) or not rng.is_contiguous():
+        _fits(rng, "rng", dtype, (2,), dev)
     return rng.data_ptr()
 
 
 def _run(what, dev, fn, *args):
     """fn(*args, stream) on device dev and its current stream."""
-    torch = _torch
-    if dev == torch._C._cuda_getDevice():
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if dev == _current_device():
+        st = fn(*args, _raw_stream(dev))
     else:
-        with torch.cuda.device(dev):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+        with _torch.cuda.device(dev):
+            st = fn(*args, _raw_stream(dev))
     if st != 0:
         raise MrnError(st, what)
 
 
 def _stats(mean, rstd, rows, dev):
     """Pointers of the row statistics; both or neither."""
-    torch = _torch
     if mean is None and rstd is None:
         return 0, 0
     if mean is None or rstd is None:
         raise ValueError("mean and rstd are given together or not at all")
-    for t, name in ((mean, "mean"), (rstd, "rstd")):
-        if t.dtype != torch.float32 or t.get_device() != dev or t.numel() != rows or \
-                not t.is_contiguous():
-            _check(t, name, torch.float32)
-            raise ValueError(f"{name} must hold one value per row ({rows}) on cuda:{dev}")
-        if t.requires_grad:
-            _no_history(t, name)
-    return mean.data_ptr(), rstd.data_ptr()
+    return _statistic(mean, "mean", rows, dev), _statistic(rstd, "rstd", rows, dev)
+
+
+def _statistic(t, name, rows, dev):
+    if t.dtype != _torch.float32 or t.get_device() != dev or t.numel() != rows or \
+            not t.is_contiguous():
+        _check(t, name, _torch.float32)
+        raise ValueError(f"{name} must hold one value per row ({rows}) on cuda:{dev}")
+    if t.requires_grad:
+        _no_history(t, name)
+    return t.data_ptr()
 
 
 def _row_output(t, name, x, dev):
@@ -640,6 +650,7 @@ def layernorm(x, gamma, beta, eps: float, out=None, mean=None, rstd=None):
     out = _row_output(out, "out", x, dev)
     _run("mrn_layernorm", dev, lib().mrn_layernorm, x.data_ptr(), gamma.data_ptr(),
          0 if beta is None else beta.data_ptr(), out.data_ptr(), pm, pr, rows, n, eps, dt)
+    _written((out,) if mean is None else (out, mean, rstd))
     return out
 
 
@@ -655,6 +666,7 @@ def dropout_add(x, residual, p: float, rng, site: int = 0, out=None):
     _run("mrn_dropout_add", dev, lib().mrn_dropout_add, x.data_ptr(),
          0 if residual is None else residual.data_ptr(), out.data_ptr(), _rng_ptr(rng, dev, p),
          site, p, rows, n, dt)
+    _written((out,))
     return out
 
 
@@ -676,6 +688,7 @@ def dropout_add_layernorm(x, residual, gamma, beta, eps: float, p: float, rng, s
          residual.data_ptr(), gamma.data_ptr(), 0 if beta is None else beta.data_ptr(),
          out_stream.data_ptr(), normed.data_ptr(), pm, pr, _rng_ptr(rng, dev, p), site, p, rows,
          n, eps, dt)
+    _written((out_stream, normed) if mean is None else (out_stream, normed, mean, rstd))
     return out_stream, normed
 
 
@@ -711,6 +724,7 @@ def layernorm_backward(dy, x, gamma, mean, rstd, dstream=None, dx=None, dgamma=N
     _run("mrn_layernorm_backward", dev, lib().mrn_layernorm_backward, dy.data_ptr(),
          x.data_ptr(), gamma.data_ptr(), pm, pr, pd, dx.data_ptr(), dgamma.data_ptr(),
          0 if dbeta is None else dbeta.data_ptr(), ws.data_ptr(), ws.numel(), rows, n, dt)
+    _written((dx, dgamma) if dbeta is None else (dx, dgamma, dbeta))
     return dx, dgamma, dbeta
 
 
@@ -729,6 +743,7 @@ def dropout_add_layernorm_backward(dnormed, out_stream, gamma, mean, rstd, p: fl
          dnormed.data_ptr(), out_stream.data_ptr(), gamma.data_ptr(), pm, pr, pd, dx.data_ptr(),
          dresidual.data_ptr(), dgamma.data_ptr(), 0 if dbeta is None else dbeta.data_ptr(),
          _rng_ptr(rng, dev, p), site, p, ws.data_ptr(), ws.numel(), rows, n, dt)
+    _written((dx, dresidual, dgamma) if dbeta is None else (dx, dresidual, dgamma, dbeta))
     return dx, dresidual, dgamma, dbeta
 
 
@@ -741,4 +756,5 @@ def rmsnorm_backward(dy, x, gamma, eps: float, dstream=None, dx=None, dgamma=Non
     _run("mrn_rmsnorm_backward", dev, lib().mrn_rmsnorm_backward, dy.data_ptr(), x.data_ptr(),
          gamma.data_ptr(), pd, dx.data_ptr(), dgamma.data_ptr(), ws.data_ptr(), ws.numel(), rows,
          n, eps, dt)
+    _written((dx, dgamma))
     return dx, dgamma

@@ -107,3 +107,39 @@ def test_from_an_autograd_function():
         assert float((u.double() - v).abs().max()) <= 512 * ref.U * float(v.abs().max())
     with pytest.raises(ValueError, match="requires a gradient"):
         torch.autograd.grad(y, leaves, t["dy"].requires_grad_(), create_graph=True)
+
+
+WRITTEN = {"layernorm": ("out", "mean", "rstd"), "dropout_add": ("out",),
+           "dropout_add_layernorm": ("out", "out2", "mean", "rstd"),
+           "layernorm_backward": ("out", "dgamma", "dbeta"),
+           "dropout_add_layernorm_backward": ("out", "out2", "dgamma", "dbeta"),
+           "rmsnorm_backward": ("out", "dgamma")}
+
+
+@pytest.mark.parametrize("name", WRITTEN)
+def test_what_a_call_writes_counts_as_modified(name):
+    """... and what it reads does not; tensors of inference mode, which have no count, are taken."""
+    call, _ = CALLS[name]
+    t = operands()
+    before = {k: v._version for k, v in t.items()}
+    call(t)
+    for k, v in t.items():
+        assert (v._version > before[k]) == (k in WRITTEN[name]), k
+    with torch.inference_mode():
+        want = flat(call(operands()))
+    assert all(torch.equal(a, b) for a, b in zip(flat(call(operands())), want))
+
+
+def test_autograd_notices_a_call_in_place():
+    """exp keeps its result for its gradient; a call that overwrites it makes the gradient an
+    error, as torch's own operations in place do."""
+    t = operands()
+    leaf = t["x"].requires_grad_()
+    for write in (lambda v: mrn.layernorm(v, t["gamma"], t["beta"], EPS, out=v),
+                  lambda v: mrn.dropout_add(v, t["residual"], P, t["rng"], out=v),
+                  lambda v: mrn.rmsnorm_backward(t["dy"], v, t["gamma"], EPS, dx=v)):
+        y = leaf.exp()
+        with torch.no_grad():
+            write(y)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.sum().backward()
