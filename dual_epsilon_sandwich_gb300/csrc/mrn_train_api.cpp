@@ -54,6 +54,10 @@ struct Buffers {
 
 enum { kRowIn = 0, kIn = 1, kRowOut = 2, kOut = 3 };
 
+// Whether a row's f32 statistic for every row fits 64 bits of bytes (rows * n * size may, at bf16
+// and n = 1, where this does not).
+bool statistics_fit(int64_t rows) { return rows <= INT64_MAX / 4; }
+
 // The dropout's threshold on the grid of 2^-16, and its scale.
 mrn_status drop_args(double p, const uint64_t *rng, uint64_t site, DropArgs *d) {
     if (!(p >= 0.0 && p <= 1.0)) return MRN_ERR_INVALID_EPS;
@@ -86,6 +90,7 @@ mrn_status backward(BackwardCall &c, cudaStream_t stream) {
     BackwardArgs &a = c.a;
     int64_t needed = 0;
     mrn_status st = check_common(a.rows, a.n, c.dtype, a.eps, a.eps);
+    if (st == MRN_OK && !statistics_fit(a.rows)) st = MRN_ERR_INVALID_SIZE;
     if (st == MRN_OK) st = workspace_bytes_needed(a.rows, a.n, &needed);
     if (st != MRN_OK) return st;
     Buffers b;
@@ -123,6 +128,7 @@ mrn_status backward(BackwardCall &c, cudaStream_t stream) {
 mrn_status layernorm(LayernormArgs &a, bool add, mrn_dtype dtype, cudaStream_t stream) {
     mrn_status st = check_common(a.rows, a.n, dtype, a.eps, a.eps);
     if (st != MRN_OK || a.rows == 0) return st;
+    if (!statistics_fit(a.rows)) return MRN_ERR_INVALID_SIZE;
     Buffers b;
     const int64_t e = elem_bytes(dtype);
     const int64_t row_bytes = a.rows * a.n * e;
