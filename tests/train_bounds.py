@@ -6,9 +6,10 @@ kernel for any width: n / 512 elements), one addition joins them, one adds the s
 a row's end; then 5 levels over a warp, at most 8 additions over the warps of a CTA and 5 levels
 over a cluster: at most 40 + n / 512 additions on the way of any term.
 
-A sum over rows: the rows of one thread (rows over the partial rows, of which there are 8 or
-more where there are as many rows), the up to 128 rows that share a CTA, a warp's share of the
-at most 1216 partial rows (16 warps or more), its 32 warps: at most 240 + rows / 8.
+A sum over rows: the rows of one thread (of rows over eight clusters or more, or over more
+CTAs), the up to 128 rows that share a CTA, a warp's share of the at most 608 partial rows (four
+for each of 152 SMs, over 16 warps or more), then up to 32 warps: 1 + rows / 8 + 128 + 38 + 32,
+at most 240 + rows / 8.
 """
 import numpy as np
 
@@ -44,3 +45,40 @@ def layernorm(x, gamma, beta, eps):
     tol = 1.01 * np.abs(gamma) * (rstd * dm + np.abs(h) * (rel + 2 * U))
     tol = tol + U * (np.abs(y) + tol)
     return (y, mean[:, 0], rstd[:, 0]), (tol, dm[:, 0], (rstd * rel)[:, 0])
+
+
+def layernorm_backward(dy, x, gamma, mean, rstd, dstream=None):
+    """((dx, dgamma, dbeta), their bounds), from the forward's f32 mean and rstd.  xh carries two
+    roundings, w one, a sum c and a product's three, the means' factors three more: c + 12 in
+    all of what dx adds up; xh and its product three in a sum over rows."""
+    rows, n = x.shape
+    rstd = rstd[:, None]
+    return _backward(dy, (x - mean[:, None]) * rstd, gamma, rstd, dstream, chain(n) + 12,
+                     row_chain(rows) + 4, row_chain(rows), True)
+
+
+def rmsnorm_backward(dy, x, gamma, eps, dstream=None):
+    """((dx, dgamma), their bounds).  inv carries half of its sum's c + 3 roundings and rsqrt's
+    two steps, c / 2 + 6; what dx adds up has it three times, beside a sum and seven products."""
+    rows, n = x.shape
+    c = chain(n)
+    inv = 1.0 / np.sqrt((x * x).mean(1, keepdims=True) + eps)
+    (dx, dg, _), (tdx, tdg, _) = _backward(dy, x * inv, gamma, inv, dstream, 2.5 * c + 28,
+                                           row_chain(rows) + c / 2 + 10, 0, False)
+    return (dx, dg), (tdx, tdg)
+
+
+def _backward(dy, xh, gamma, rstd, dstream, roundings, gamma_roundings, beta_roundings, centred):
+    w = dy * gamma
+    c1 = w.mean(1, keepdims=True) if centred else np.zeros_like(rstd)
+    c2 = (w * xh).mean(1, keepdims=True)
+    ds = rstd * (w - c1 - xh * c2)
+    parts = np.abs(w) + np.abs(w).mean(1, keepdims=True) * centred \
+        + np.abs(xh) * np.abs(w * xh).mean(1, keepdims=True)
+    tol = 1.01 * U * roundings * rstd * parts
+    if dstream is not None:
+        ds = ds + dstream
+        tol = tol + U * np.abs(ds)
+    return ((ds, (dy * xh).sum(0), dy.sum(0)),
+            (tol, 1.01 * U * gamma_roundings * np.abs(dy * xh).sum(0),
+             1.01 * U * beta_roundings * np.abs(dy).sum(0)))
