@@ -13,6 +13,8 @@ namespace mrn {
 constexpr int kLoopedThreads = 512;
 // Threads that an SM's registers are shared between (the launch bound), from what a thread
 // holds: k slots of r rows and of two weights.
+// It does not count what rows that share a warp take beside them (distances of their own, with
+// ends one more generator group): ten of those bf16 forms spill, 4 to 96 bytes.
 template <class T> constexpr int forward_resident(int k, int r) {
     const int words = k * (r + 2) * Slot<T>::kWords;
     return words <= 12 ? 1024 : (words <= 28 ? 768 : (words <= 36 ? 640 : (words <= 68 ? 512 : (words <= 100 ? 384 : 256))));
@@ -26,9 +28,9 @@ template <class T> constexpr int forward_threads(int k, int r) {
 // nearest: Markstein's step ("Computation of elementary functions on the IBM RISC System/6000
 // processor", 1990).  q is within one and a half units of the quotient; what the fma leaves of
 // sum is a whole multiple of q's unit, of at most 1.5 n units, and exact; times inv it takes q to
-// within 2^-23 units of the quotient.  A quotient by n <= 2^18 (all that the row tiles hold) lies
-// 2^-19 units at least from the border between two f32 numbers, so that the last addition rounds
-// as the quotient itself would be rounded.
+// within 2^-23 units of the quotient.  A quotient by n < 2^19 (the row tiles hold up to 2^18
+// elements and the ends) lies 2^-20 units at least from the border between two f32 numbers, so
+// that the last addition rounds as the quotient itself would be rounded.
 //   The product alone missed it by up to a unit: a constant row of 1000.0, n = 6656, whose sum is
 // exact, came out 0.02 off beta at eps 1e-5 and 0.5 off at 1e-8.  Every row waits for this; measured
 // on GB300, us with the product, so, and with a division: f32 8192 x 4096 45.8, 46.6, 47.5, bf16
@@ -88,9 +90,9 @@ __global__ void __launch_bounds__(kLoopedThreads) mrn_layernorm_looped_kernel(co
 
 // Rows held in registers between their copy and their outputs (see mrn_row_tile.cuh): the
 // deviations are taken from the values themselves, so that every operand is read once and every
-// output written once.  Measured on GB300: 16384 x 4096 bf16 44.5 us alone (6.0 TB/s, 89 % of
-// the copy's rate) and 88.7 after the add (6.1 TB/s); 4096 x 6655 f32 after the add 76.1 us
-// (5.7 TB/s); 4 x 6656 f32 2.5 us, a launch and two sums over a cluster.
+// output written once.  Measured on GB300: 16384 x 4096 bf16 45.7 us alone (5.9 TB/s, 87 % of
+// the copy's rate) and 90.1 after the add (6.0 TB/s); 4096 x 6655 f32 after the add 77.7 us
+// (5.6 TB/s); 4 x 6656 f32 2.6 us, a launch and two sums over a cluster.
 //   What bounds it: not memory alone (dram 69 % busy under ncu) but the instructions of 16 warps
 // on an SM, issued in 55 % of cycles, with the generator's and the conversions' the most of
 // them; a row's two sums, each a barrier of its CTA, are covered by the copies in flight and
@@ -254,25 +256,36 @@ bool launch_layernorm_k(const LayernormArgs &a, const TileShape &p, int sms, boo
 }
 
 // Slots per thread (k) and rows at a time (r) for rows of a CTA.  Measured on GB300, a call of
-// 220 MB (alone) or 440 MB (after the add), k x r (us):
-//   bf16 alone      n = 1536 2 x 2 45.9, 4 x 1 48.1;  2048 4 x 1 45.2, 2 x 2 45.3;  4096 4 x 1
-//                   44.4, 2 x 2 47.2;  4095 4 x 1 50.2, 2 x 2 61;  8192 4 x 1 43, 2 x 2 50
-//   bf16 after add  n = 2048 4 x 1 94.4;  4096 2 x 2 89.9, 4 x 1 93;  4095 4 x 1 90.5, 2 x 2
-//                   111;  5120 4 x 1 88, 2 x 2 89;  8192 4 x 1 86, 2 x 2 88
-//   f32 alone       n = 4096 1 x 1 43, 4 x 1 45;  6656 2 x 2 38.9, 4 x 1 40;  6655 2 x 2 42.1, 4
-//                   x 1 46.2;  12288 4 x 1 50, 2 x 1 58
-//   f32 after add   n = 4096 1 x 1 63, 4 x 2 65;  5120 2 x 1 72.3, 4 x 1 76.2;  6655 2 x 1 75.9,
-//                   4 x 1 79;  6656 4 x 1 72.0, 2 x 1 73;  8191 4 x 1 77.7, 2 x 1 79
+// 269 MB (alone) or 537 MB (after the add), k x r (us):
+//   bf16 alone      n = 1280 2 x 2 49.0, 4 x 1 54.2;  1408 49.7, 51.3;  1536 50.0, 49.2;  2048 49.6,
+//                   47.4;  4096 46.9, 45.9;  4095 59.0, 51.3;  8192 55.5, 46.2
+//   bf16 after add  n = 1280 2 x 2 96.7, 4 x 1 108.1;  1536 97.1, 92.5;  2048 95.6, 94.5;  2568
+//                   102.7, 94.5;  3584 94.8, 91.0;  3712 94.8, 92.2;  3840 92.8, 93.3;  3968 92.2,
+//                   93.8;  4096 90.2, 94.3;  4104 110.9, 105.3;  4608 98.6, 94.5;  5120 96.1,
+//                   91.4;  8192 102.2, 89.9;  odd: 4095 115.2, 90.2
+//   f32 alone       n = 2048 1 x 1 49.1, 2 x 1 47.2;  4096 1 x 1 46.9, 2 x 1 46.8, 4 x 1 47.1;
+//                   4104 2 x 2 54.4, 2 x 1 48.9;  6656 2 x 2 47.5, 2 x 1 46.3, 4 x 1 52.4;  6655
+//                   52.4, 61.6, 56.6;  8192 47.6, 48.2, 49.3;  8200 72.8, 62.2, 54.4;  12288 58.5,
+//                   61.0, 48.2
+//   f32 after add   n = 2048 1 x 1 92.2, 2 x 1 91.2;  4096 92.2, 92.5;  4104 2 x 1 96.6, 4 x 1 100.9;
+//                   5120 92.5, 92.8;  6655 92.6, 100.8;  6656 94.5, 88.4;  7168 93.7, 87.2;  7176
+//                   100.7, 94.3;  8191 98.4, 93.5;  8192 93.8, 92.2
+// Where a border serves aligned and odd widths, the odd ones, which lose more, set it (f32 6655 beside
+// 6656).
 // Rows in clusters, and their CTAs' threads (us): f32 alone 4096 x 16384 2 x 2 of 128 98.8, 2 x 1
-// of 512 104.7, 4 x 1 of 384 132; 2048 x 32768 2 x 1 of 256 107, 2 x 2 of 128 115.  f32 after add
-// 4096 x 16384 2 x 1 of 256 176, 4 x 1 198.  bf16 alone 2048 x 32768 4 x 1 of 128 66, of 512 72.
+// of 512 104.7, 4 x 1 of 384 132, but 2048 x 16384 59.6, 59.0, 65.7 and 2 x 1 of 256 51.8; 1024 x
+// 32768 2 x 1 of 256 54.7, of 512 62.4, 2 x 2 of 256 62.4; 512 x 65536 2 x 1 of 256 71.1, of 512
+// 72.7, 2 x 2 of 256 67.5, 4 x 1 of 384 67.7.  f32 after add 2048 x 16384 2 x 1 of 256 91.7, of 128
+// 88.4, of 512 94.3, 4 x 1 of 256 98.4; 512 x 65536 2 x 1 of 256 115.8, of 512 118.9.  bf16 4 x 1
+// alone 3276 x 20480 of 128 64.3, of 256 74.6; 2048 x 32768 of 128 72.6, of 256 66.5, of 512 68.7;
+// 1024 x 65536 90.9, 80.0, 73.8; after add the last two 101.2, 114.3, 113.2 and 115.2, 119.1, 122.7.
 template <class T> void forward_tile(int64_t slots, bool add, bool edge, int *k, int *r, int *threads) {
     if (T::kBytes == 4 && slots > 1536) {
         *k = 2;
         *r = !add && slots <= 2048 ? 2 : 1;
         *threads = *r == 2 ? 128 : 256;
     } else if (T::kBytes == 2) {
-        const bool two = slots <= 192 || (add && !edge && slots > 320 && slots <= 576);
+        const bool two = slots < 192 || (add && !edge && slots > 464 && slots <= 512);
         *k = two ? 2 : 4;
         *r = two ? 2 : 1;
     } else if (add) {

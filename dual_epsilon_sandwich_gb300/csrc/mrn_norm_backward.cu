@@ -100,9 +100,9 @@ mrn_norm_backward_looped_kernel(const BackwardArgs a, float *part_gamma, float *
 // registers over all rows of the CTA (see mrn_row_tile.cuh).  Each operand is read once, and
 // both sums of a row are taken together, so a row costs one barrier.  Measured on GB300, with
 // the join: 16384 x 4096 bf16 76 us (5.3 TB/s, 78 % of the copy's rate), with dropout and a
-// stream's gradient 121 us (5.6 TB/s); 16384 x 4095 bf16 with both 138 us (4.9 TB/s); 4096 x
-// 6656 f32 with both 92 us (5.9 TB/s); RMSNorm 163840 x 128 bf16 24 us (5.2 TB/s), 4096 x 16384
-// f32 in clusters 178 us (6.0 TB/s).
+// stream's gradient 121 us (5.5 TB/s); 16384 x 4095 bf16 with both 139 us (4.8 TB/s); 4096 x
+// 6656 f32 with both 95 us (5.7 TB/s); RMSNorm 163840 x 128 bf16 24 us (5.2 TB/s), 4096 x 16384
+// f32 in clusters 178 to 188 us on several GPUs (5.7 to 6.0 TB/s).
 //   What bounds it: the instructions of the 16 warps that the registers of the column sums leave
 // room for (issued in 54 % of cycles under ncu, dram 60 to 65 % busy; waits for shared memory
 // and for results of arithmetic come first), then the join with its launch, 4 to 6 us.  Where
@@ -453,8 +453,9 @@ cudaError_t launch_join_typed(const JoinArgs &a, bool pdl, cudaStream_t stream, 
 }
 
 cudaError_t launch_join(const JoinArgs &a, bool pdl, cudaStream_t stream, uint64_t *launches) {
-    // (measured on GB300, us a call: 163840 x 128 bf16, 1216 partial rows, 25.3 with 32 warps
-    // of 32 columns against 27.2 with 16 of 64; 16384 x 4096 bf16 71.2 against 70.0)
+    // (measured on GB300, us a call with 608 partial rows, 32 warps of 32 columns against 16 of 64:
+    // 163840 x 128 bf16 24.2, 26.0;  65536 x 1024 bf16 71.0, 71.7;  32768 x 2048 80.0, 81.5;  16384 x
+    // 4096 76.3, 75.8;  4096 x 6656 f32 61.9, 59.1)
     return a.n <= 1024 ? launch_join_typed<32, 1, 20>(a, pdl, stream, launches)
                        : launch_join_typed<16, 2, 10>(a, pdl, stream, launches);
 }
@@ -475,23 +476,36 @@ cudaError_t launch_backward_typed(const BackwardArgs &a, int sms, bool pdl, cuda
     bool done = false;
     // (a generator group is a slot only when the operands start on a slot boundary)
     if (mis == 0 || (mis > 0 && a.drop.threshold == 0)) {
-        // Slots per thread (k) for rows of a CTA, and threads of one at most.  Measured on GB300, a
-        // call of 400 to 670 MB (us), with dropout where not said otherwise:
-        //   bf16  n = 4096 2 121.0, 3 125.2, 4 125.5;  4095 2 145.5, 4 151.7;  6656 4 133.7, 2
-        //         137.4;  6655 4 149.5, 2 163.9;  8192 4 129.0, 2 131.2;  without dropout 8191
-        //         2 96.4, 4 99.3;  16384 in clusters of CTAs of 64 threads 4 111, of 128 118
-        //   f32   n = 4096 3 84.2, 2 93.7, 4 94.4;  4095 4 95.3, 2 99.3, 3 113.0;  6656 4 94.9, 3
-        //         100.9;  6655 4 99.3, 2 106.8, 3 112.3;  8191 4 101.1, 3 121.4;  16384 in
-        //         clusters of CTAs of 256 threads 4 218, 2 224, of 64 4 221;  16383 of 64 4
-        //         230, of 256 4 250;  rmsnorm 12288 4 133, 2 of 512 137;  16384 4 183, 2 of 512
-        //         175;  24576 4 136, 2 of 512 148
+        // Slots per thread (k) for rows of a CTA, and threads of one at most.  Measured on GB300 (us),
+        // with dropout and a stream's gradient 671 MB a call, LayerNorm's alone ("ln") 403 MB:
+        //   bf16  n = 1536 2 119.1, 4 125.2;  2048 126.5, 117.6;  2560 126.3, 137.7;  4095 139.1,
+        //         141.1;  4096 121.2, 117.0;  5120 141.6, 145.5;  5632 136.5, 140.1;  6656 139.6,
+        //         135.2;  6655 161.0, 149.6;  8192 130.9, 129.1;  ln: 2559 83.0, 104.5;  4096 76.6,
+        //         80.2;  4095 86.1, 84.6;  5120 91.9, 90.4;  6656 88.1, 84.3;  8191 94.0, 88.4;
+        //         rmsnorm with a stream's gradient 5120 102.5, 110.9;  8192 94.3, 98.4;  rows of
+        //         16384 in clusters of CTAs of 64 threads 4 129.3, of 128 135.5, of 256 145.5
+        //   f32   n = 1152 3 122.4, 4 133.7;  1280 126.0, 123.7;  1536 125.8, 118.9;  1792 121.9,
+        //         124.0;  2048 122.4, 125.8;  2304 123.0, 113.0;  2560 121.0, 113.2;  2816 121.6,
+        //         120.4;  3328 122.2, 123.9;  4096 110.9, 125.4;  4104 122.4, 133.3;  4480 115.5,
+        //         116.6;  4608 119.6, 114.8;  5120 121.2, 113.7;  6656 123.3, 116.2;  ln: 1408 83.0,
+        //         74.0;  1544 81.5, 82.0;  2560 79.3, 73.6;  4352 77.9, 82.3;  odd widths 2047 2
+        //         128.9, 4 132.4;  2559 131.1, 125.3;  4095 2 131.2, 3 152.4, 4 125.8;  5119 2
+        //         119.1, 4 127.3;  6655 2 119.6, 3 133.2, 4 119.1;  8191 3 145.7, 4 121.4
+        //         16384 in clusters of CTAs of 256 threads 4 117.8, 2 120.4, of 64 4 118.3;  16383
+        //         of 64 123.0, of 256 135.8;  rmsnorm with a stream's gradient (537 MB) 12288 4 93.0,
+        //         2 of 512 96.1;  16384 99.4, 94.9;  24576 of 128 94.8, 2 of 512 102.7;  32768 of 128
+        //         96.3, of 256 98.4;  65536 of 128 117.6, of 256 114.0, 2 of 512 117.3
+        // bf16: two slots also where four win at aligned widths only (2048, 4096): beside them, and at
+        // odd widths, four lose more.
         const int64_t slots = a.n / 8;
         const bool edge = mis != 0 || a.n % 8 != 0;
         int k;
         if (T::kBytes == 2) {
             k = slots > 1024 || (a.dres && slots > 640) ? 4 : 2;
         } else {
-            k = edge || slots > 512 ? 4 : 3;
+            const bool four = edge || slots > 560 || (slots >= 160 && slots <= 192) ||
+                              (slots > 256 && slots <= 352);
+            k = four ? 4 : 3;
         }
         int most_threads = backward_resident(k);
         if (slots > 1024 && (T::kBytes == 2 || edge || slots > 2048))

@@ -9,8 +9,8 @@
 //    dropout's generator groups.  When the row pitch is not a multiple of eight (EDGE),
 //    up to seven elements before the row's first whole slot and seven behind its last are
 //    taken one by one, each by a lane of its own: every slot is whole, and only the warp
-//    that holds the ends does more (16384 x 4095 bf16, the gradient: 79 us without that
-//    work, 91 with it, 118 with masked slots instead).
+//    that holds the ends does more (16384 x 4095 bf16, the gradient: 86 us, where 4096 takes 76;
+//    when it was chosen 91, 79 without that work, 118 with masked slots instead).
 //    The rows of one CTA are a multiple of eight apart, so that they all start alike and
 //    a thread's columns stay the same: weights are loaded once, and column sums stay in
 //    registers over all rows.

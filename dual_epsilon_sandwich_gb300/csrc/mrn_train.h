@@ -10,7 +10,7 @@
 namespace mrn {
 
 // The dropout of one call: element e of the flattened [rows x n] matrix is
-// kept when its 16 random bits are >= threshold (see philox_lanes in
+// kept when its 16 random bits are >= threshold (see drop_groups and DropGroup in
 // mrn_train_kernels.cuh), and kept values are multiplied by scale.
 struct DropArgs {
     const uint64_t *rng;    // device: {seed, offset}; not read when threshold == 0
@@ -45,7 +45,7 @@ struct BackwardArgs {
     void *dx;                   // with dres: dropout(ds); else ds
     void *dres;                 // NULL: no dropout follows
     float *dgamma, *dbeta;      // dbeta NULL: none
-    float *workspace;           // [parts x n] partial sums of dgamma, then of dbeta
+    float *workspace;           // [parts x part_stride_of(n)] partial sums of dgamma, then of dbeta
     DropArgs drop;
     int64_t rows, n;
     float eps;                  // RMSNorm
