@@ -248,8 +248,10 @@ mrn_status mrn_seam_scale(const void *u, const void *gamma, void *y, int64_t row
  * of a row whose pitch is not a multiple of eight go one by one (bf16: the four bytes
  * that hold the element are read, which may take in one element beside the row, never
  * more).  Operands at different offsets, rows wider than a cluster of CTAs holds (over
- * 131,072 elements) and, with a dropout, operands off a multiple of eight go element by
- * element: several times slower, with the same meaning.
+ * 131,072 elements; 262,144 in a bf16 forward) and, with a dropout, operands off a multiple
+ * of eight go element by element: several times slower, with the same meaning.  Sums are
+ * then taken in another order: such a call and one with operands elsewhere agree within
+ * roundings, not bit for bit.
  * Launches: one kernel per call, two for a gradient with weights (the rows, then the
  * sum of what the CTAs left of dgamma and dbeta); mrn_force_geometry does not apply.
  * Rows that are split over a cluster wait for each other for about a second at most;
