@@ -6,9 +6,12 @@ handle as an int (0 = legacy default stream), and each returns the
 ``mrn_status`` code.  ``rmsnorm``, ``rmsnorm_then_add`` and
 ``norm_residual_norm`` are conveniences for torch CUDA tensors: they read
 pointers, sizes, dtype and the current stream off the tensors, call the C ABI
-and raise ``MrnError`` on a non-zero status.  Every step of the computation
-runs in the library's CUDA kernels; there is no other code path.  If
-``libmrn.so`` has not been built, every call raises.
+and raise ``MrnError`` on a non-zero status.  What they return has no autograd
+history; the training helpers (``layernorm``, ``dropout_add``,
+``dropout_add_layernorm`` and the ``*_backward``) refuse a tensor that requires a
+gradient while autograd records.  Every step of the computation runs in the
+library's CUDA kernels; there is no other code path.  If ``libmrn.so`` has not
+been built, every call raises.
 """
 from __future__ import annotations
 
