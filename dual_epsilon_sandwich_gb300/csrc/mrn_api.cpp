@@ -872,8 +872,8 @@ const char *mrn_status_string(mrn_status status) {
     switch (status) {
     case MRN_OK: return "ok";
     case MRN_ERR_NULL_POINTER: return "a required pointer is NULL";
-    case MRN_ERR_INVALID_SIZE: return "invalid size (n < 1, rows < 0, byte size overflow or workspace too small)";
-    case MRN_ERR_INVALID_EPS: return "eps must be finite and > 0 (a dropout probability 0 .. 1)";
+    case MRN_ERR_INVALID_SIZE: return "invalid size (n < 1, rows < 0, byte size overflow, workspace too small, tensors or elements < 0, or a factor of no known kind)";
+    case MRN_ERR_INVALID_EPS: return "eps must be finite and > 0 (a dropout probability 0 .. 1, a largest norm >= 0)";
     case MRN_ERR_UNSUPPORTED_DTYPE: return "unsupported dtype";
     case MRN_ERR_ALIASING: return "forbidden overlap between buffers";
     case MRN_ERR_MISALIGNED: return "pointer not aligned to its element size";

@@ -1,5 +1,5 @@
 // mrn_checks.h -- argument checks shared by the C entry points (mrn_api.cpp,
-// mrn_train_api.cpp), and what both need of the launch state.  Host only; not
+// mrn_train_api.cpp, mrn_gate_api.cpp), and what they need of the launch state.  Host only; not
 // part of the public ABI.
 #pragma once
 
@@ -40,6 +40,45 @@ inline mrn_status check_common(int64_t rows, int64_t n, mrn_dtype dt, float eps1
 }
 
 inline bool aligned_to(const void *p, int64_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+// The buffers of one call, collected to be checked against each other.
+struct Buffers {
+    struct Entry {
+        Span span;
+        int role;   // 0: row input, 1: other input, 2: row output, 3: other output
+    };
+    Entry e[20];
+    int count = 0;
+    bool missing = false;
+    bool misaligned = false;
+
+    void add(int role, const void *p, int64_t bytes, int64_t align, bool optional = false) {
+        if (!p) {
+            missing = missing || !optional;
+            return;
+        }
+        misaligned = misaligned || !aligned_to(p, align);
+        e[count++] = Entry{span_of(p, bytes), role};
+    }
+    // A row output may be a row input itself; every other overlap with an output is refused.
+    mrn_status check() const {
+        if (missing) return MRN_ERR_NULL_POINTER;
+        if (misaligned) return MRN_ERR_MISALIGNED;
+        for (int i = 0; i < count; ++i) {
+            if (e[i].role < 2) continue;
+            for (int k = 0; k < count; ++k) {
+                if (k == i) continue;
+                const bool may_be_same = e[i].role == 2 && e[k].role == 0;
+                if (may_be_same ? !output_vs_row_input_ok(e[i].span, e[k].span)
+                                : overlaps(e[i].span, e[k].span))
+                    return MRN_ERR_ALIASING;
+            }
+        }
+        return MRN_OK;
+    }
+};
+
+enum { kRowIn = 0, kIn = 1, kRowOut = 2, kOut = 3 };
 
 // SM count of the current device (GB300's where it cannot be asked).
 int sm_count_of_current_device();

@@ -15,45 +15,6 @@ namespace {
 
 using namespace mrn;
 
-// The buffers of one call, collected to be checked against each other.
-struct Buffers {
-    struct Entry {
-        Span span;
-        int role;   // 0: row input, 1: other input, 2: row output, 3: other output
-    };
-    Entry e[16];
-    int count = 0;
-    bool missing = false;
-    bool misaligned = false;
-
-    void add(int role, const void *p, int64_t bytes, int64_t align, bool optional = false) {
-        if (!p) {
-            missing = missing || !optional;
-            return;
-        }
-        misaligned = misaligned || !aligned_to(p, align);
-        e[count++] = Entry{span_of(p, bytes), role};
-    }
-    // A row output may be a row input itself; every other overlap with an output is refused.
-    mrn_status check() const {
-        if (missing) return MRN_ERR_NULL_POINTER;
-        if (misaligned) return MRN_ERR_MISALIGNED;
-        for (int i = 0; i < count; ++i) {
-            if (e[i].role < 2) continue;
-            for (int k = 0; k < count; ++k) {
-                if (k == i) continue;
-                const bool may_be_same = e[i].role == 2 && e[k].role == 0;
-                if (may_be_same ? !output_vs_row_input_ok(e[i].span, e[k].span)
-                                : overlaps(e[i].span, e[k].span))
-                    return MRN_ERR_ALIASING;
-            }
-        }
-        return MRN_OK;
-    }
-};
-
-enum { kRowIn = 0, kIn = 1, kRowOut = 2, kOut = 3 };
-
 // Whether a row's f32 statistic for every row fits 64 bits of bytes (rows * n * size may, at bf16
 // and n = 1, where this does not).
 bool statistics_fit(int64_t rows) { return rows <= INT64_MAX / 4; }

@@ -8,8 +8,8 @@ handle as an int (0 = legacy default stream), and each returns the
 pointers, sizes, dtype and the current stream off the tensors, call the C ABI
 and raise ``MrnError`` on a non-zero status.  What they return has no autograd
 history; the training helpers (``layernorm``, ``dropout_add``,
-``dropout_add_layernorm`` and the ``*_backward``) refuse a tensor that requires a
-gradient while autograd records.  Every step of the computation runs in the
+``dropout_add_layernorm``, ``norm_gate_residual_norm``, the ``*_backward``, ``grad_norm`` and
+``clip_grad_norm``) refuse a tensor that requires a gradient while autograd records.  Every step of the computation runs in the
 library's CUDA kernels; there is no other code path.  If ``libmrn.so`` has not
 been built, every call raises.
 """
@@ -35,6 +35,11 @@ MRN_OP_RMSNORM_Q8_1 = 5
 MRN_OP_RMSNORM_SEAM = 6
 MRN_OP_RMSNORM_UNWEIGHTED = 7
 Q8_1_BLOCK_BYTES = 36
+
+MRN_FACTOR_NONE = 0
+MRN_FACTOR_SCALAR = 1
+MRN_FACTOR_CHANNEL = 2
+MRN_FACTOR_ROW = 3
 
 MRN_GEOM_AUTO = 0
 MRN_GEOM_ROWS_PER_WARP = 1
@@ -67,7 +72,10 @@ EXPORTS = ("mrn_rmsnorm", "mrn_rmsnorm_then_add", "mrn_norm_residual_norm",
            "mrn_set_launch_options", "mrn_launch_options", "mrn_rmsnorm_seam",
            "mrn_rmsnorm_unweighted", "mrn_seam_scale", "mrn_layernorm", "mrn_dropout_add",
            "mrn_dropout_add_layernorm", "mrn_norm_backward_workspace", "mrn_layernorm_backward",
-           "mrn_dropout_add_layernorm_backward", "mrn_rmsnorm_backward")
+           "mrn_dropout_add_layernorm_backward", "mrn_rmsnorm_backward",
+           "mrn_norm_gate_residual_norm", "mrn_norm_gate_backward_workspace",
+           "mrn_norm_gate_residual_norm_backward", "mrn_grad_norm_workspace", "mrn_grad_norm",
+           "mrn_clip_grad_norm")
 
 
 class MrnError(RuntimeError):
@@ -133,12 +141,23 @@ def lib() -> ctypes.CDLL:
             L.mrn_dropout_add_layernorm_backward.argtypes = \
                 [_vp] * 11 + [_u64, _d, _vp, _i64, _i64, _i64, _i, _vp]
             L.mrn_rmsnorm_backward.argtypes = [_vp] * 7 + [_i64, _i64, _i64, _f, _i, _vp]
+            L.mrn_norm_gate_residual_norm.argtypes = \
+                [_vp] * 5 + [_i, _vp, _i, _vp, _vp, _i64, _i64, _f, _f, _i, _vp]
+            L.mrn_norm_gate_backward_workspace.argtypes = [_i64, _i64, ctypes.POINTER(_i64)]
+            L.mrn_norm_gate_residual_norm_backward.argtypes = \
+                [_vp] * 8 + [_i, _vp, _i] + [_vp] * 7 + [_i64, _i64, _i64, _f, _f, _i, _vp]
+            L.mrn_grad_norm_workspace.argtypes = [_i64, ctypes.POINTER(_i64)]
+            L.mrn_grad_norm.argtypes = [_vp, _vp, _vp, _i64, _vp, _vp, _i64, _vp]
+            L.mrn_clip_grad_norm.argtypes = [_vp, _vp, _vp, _vp, _i64, _d, _vp, _vp, _i64, _vp]
             for fn in (L.mrn_rmsnorm, L.mrn_rmsnorm_then_add, L.mrn_norm_residual_norm,
                        L.mrn_add_rmsnorm, L.mrn_rmsnorm_then_add_scale, L.mrn_rmsnorm_q8_1,
                        L.mrn_rmsnorm_seam, L.mrn_rmsnorm_unweighted, L.mrn_seam_scale,
                        L.mrn_layernorm, L.mrn_dropout_add, L.mrn_dropout_add_layernorm,
                        L.mrn_norm_backward_workspace, L.mrn_layernorm_backward,
-                       L.mrn_dropout_add_layernorm_backward, L.mrn_rmsnorm_backward):
+                       L.mrn_dropout_add_layernorm_backward, L.mrn_rmsnorm_backward,
+                       L.mrn_norm_gate_residual_norm, L.mrn_norm_gate_backward_workspace,
+                       L.mrn_norm_gate_residual_norm_backward, L.mrn_grad_norm_workspace,
+                       L.mrn_grad_norm, L.mrn_clip_grad_norm):
                 fn.restype = _i
             L.mrn_status_string.argtypes = [_i]
             L.mrn_status_string.restype = ctypes.c_char_p
@@ -245,6 +264,61 @@ def mrn_rmsnorm_backward(dy, x, gamma, dstream, dx, dgamma, workspace, workspace
                          eps, dtype, stream=0) -> int:
     return lib().mrn_rmsnorm_backward(dy, x, gamma, dstream, dx, dgamma, workspace,
                                       workspace_bytes, rows, n, eps, dtype, stream)
+
+
+def mrn_norm_gate_residual_norm(block_out, residual, gamma_post, gamma_pre, gate, gate_kind,
+                                res_scale, res_scale_kind, out_stream, normed, rows, n, eps_post,
+                                eps_pre, dtype, stream=0) -> int:
+    return lib().mrn_norm_gate_residual_norm(
+        block_out, residual, gamma_post, gamma_pre, gate, gate_kind, res_scale, res_scale_kind,
+        out_stream, normed, rows, n, eps_post, eps_pre, dtype, stream)
+
+
+def mrn_norm_gate_backward_workspace(rows, n) -> int:
+    """Bytes of workspace that the gated tail's gradient of rows x n needs on the current device."""
+    out = ctypes.c_int64(0)
+    st = lib().mrn_norm_gate_backward_workspace(rows, n, ctypes.byref(out))
+    if st != 0:
+        raise MrnError(st, "mrn_norm_gate_backward_workspace")
+    return out.value
+
+
+def mrn_norm_gate_residual_norm_backward(dnormed, dstream, block_out, out_stream, residual,
+                                         gamma_post, gamma_pre, gate, gate_kind, res_scale,
+                                         res_scale_kind, dblock, dresidual, dgamma_post, dgamma_pre,
+                                         dgate, dres_scale, workspace, workspace_bytes, rows, n,
+                                         eps_post, eps_pre, dtype, stream=0) -> int:
+    return lib().mrn_norm_gate_residual_norm_backward(
+        dnormed, dstream, block_out, out_stream, residual, gamma_post, gamma_pre, gate, gate_kind,
+        res_scale, res_scale_kind, dblock, dresidual, dgamma_post, dgamma_pre, dgate, dres_scale,
+        workspace, workspace_bytes, rows, n, eps_post, eps_pre, dtype, stream)
+
+
+def mrn_grad_norm_workspace(tensors) -> int:
+    """Bytes of workspace that lists of up to this many tensors need on the current device."""
+    out = ctypes.c_int64(0)
+    st = lib().mrn_grad_norm_workspace(tensors, ctypes.byref(out))
+    if st != 0:
+        raise MrnError(st, "mrn_grad_norm_workspace")
+    return out.value
+
+
+def _list_arrays(grads, counts, dtypes):
+    n = len(grads)
+    return (_vp * n)(*grads), (_i64 * n)(*counts), (_i * n)(*dtypes), n
+
+
+def mrn_grad_norm(grads, counts, dtypes, norm, workspace, workspace_bytes, stream=0) -> int:
+    """grads, counts, dtypes: sequences of addresses, element counts and dtype codes."""
+    g, c, d, n = _list_arrays(grads, counts, dtypes)
+    return lib().mrn_grad_norm(g, c, d, n, norm, workspace, workspace_bytes, stream)
+
+
+def mrn_clip_grad_norm(grads, out, counts, dtypes, max_norm, norm, workspace, workspace_bytes,
+                       stream=0) -> int:
+    g, c, d, n = _list_arrays(grads, counts, dtypes)
+    return lib().mrn_clip_grad_norm(g, (_vp * n)(*out), c, d, n, max_norm, norm, workspace,
+                                    workspace_bytes, stream)
 
 
 def mrn_status_string(status: int) -> str:
@@ -761,3 +835,216 @@ def rmsnorm_backward(dy, x, gamma, eps: float, dstream=None, dx=None, dgamma=Non
          n, eps, dt)
     _written((dx, dgamma))
     return dx, dgamma
+
+
+# ---------------------------------------------------------------------------
+# The sandwich tail with a gate and a residual scale, and its gradient.  A factor's shape says
+# how it is shared: (1,) a scalar, (n,) one value per channel, x.shape[:-1] + (1,) one per row
+# (the gate only); None is one.
+# ---------------------------------------------------------------------------
+def _factor(t, name, x, n, dev, rows_too):
+    """(pointer, kind) of a factor of rows like x's."""
+    if t is None:
+        return 0, MRN_FACTOR_NONE
+    shape = t.shape
+    if shape == (1,):
+        kind = MRN_FACTOR_SCALAR
+    elif shape == (n,):
+        kind = MRN_FACTOR_CHANNEL
+    elif rows_too and shape == x.shape[:-1] + (1,):
+        kind = MRN_FACTOR_ROW
+    else:
+        _check(t, name, x.dtype)
+        expected = f"(1,), ({n},)" + (f" or {tuple(x.shape[:-1]) + (1,)}" if rows_too else "")
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected {expected}")
+    _fits(t, name, x.dtype, shape, dev)
+    return t.data_ptr(), kind
+
+
+def _factor_gradient(t, name, factor, dev):
+    """t, or a new float32 tensor of the factor's shape when it is None."""
+    if t is None:
+        return _torch.empty(factor.shape, dtype=_torch.float32, device=factor.device)
+    _fits(t, name, _torch.float32, factor.shape, dev)
+    return t
+
+
+def norm_gate_residual_norm(block_out, residual, gamma_post, gamma_pre, gate=None, res_scale=None,
+                            eps_post: float = 1e-8, eps_pre: float = 1e-5, out_stream=None,
+                            normed=None):
+    """(out_stream, normed): out_stream = res_scale * residual + gate * RMSNorm(block_out;
+    eps_post) * gamma_post, normed = RMSNorm(out_stream; eps_pre) * gamma_pre.  gate: None, (1,),
+    (n,) or one value per row, block_out.shape[:-1] + (1,); res_scale: None, (1,) or (n,).
+    out_stream may be residual (in-place update) or block_out."""
+    rows, n, dt, dev = _train_rows(block_out, "block_out")
+    if block_out.requires_grad:
+        _no_history(block_out, "block_out")
+    _fits(residual, "residual", block_out.dtype, block_out.shape, dev)
+    _fits(gamma_post, "gamma_post", block_out.dtype, (n,), dev)
+    _fits(gamma_pre, "gamma_pre", block_out.dtype, (n,), dev)
+    pg, kg = _factor(gate, "gate", block_out, n, dev, True)
+    ps, ks = _factor(res_scale, "res_scale", block_out, n, dev, False)
+    out_stream = _row_output(out_stream, "out_stream", block_out, dev)
+    normed = _row_output(normed, "normed", block_out, dev)
+    _run("mrn_norm_gate_residual_norm", dev, lib().mrn_norm_gate_residual_norm,
+         block_out.data_ptr(), residual.data_ptr(), gamma_post.data_ptr(), gamma_pre.data_ptr(),
+         pg, kg, ps, ks, out_stream.data_ptr(), normed.data_ptr(), rows, n, eps_post, eps_pre, dt)
+    _written((out_stream, normed))
+    return out_stream, normed
+
+
+def norm_gate_backward_workspace(x):
+    """Workspace (uint8 tensor) for norm_gate_residual_norm_backward over rows like x's, on x's
+    device.  Reusable by later calls of this shape on one stream; calls that may run at the same
+    time need one each."""
+    rows, n, _, dev = _train_rows(x, "x")
+    with _torch.cuda.device(dev):
+        return _torch.empty(mrn_norm_gate_backward_workspace(rows, n), dtype=_torch.uint8,
+                            device=x.device)
+
+
+def norm_gate_residual_norm_backward(dnormed, block_out, out_stream, gamma_post, gamma_pre,
+                                     gate=None, res_scale=None, residual=None,
+                                     eps_post: float = 1e-8, eps_pre: float = 1e-5, dstream=None,
+                                     dblock=None, dresidual=None, dgamma_post=None, dgamma_pre=None,
+                                     dgate=None, dres_scale=None, workspace=None):
+    """(dblock, dresidual, dgamma_post, dgamma_pre, dgate, dres_scale) of
+    norm_gate_residual_norm, from its operands and its out_stream; without factors, the gradient
+    of norm_residual_norm.  The last four are float32; dgate is None without a gate, dres_scale
+    without a res_scale or without residual (the forward's, not updated in place).  dstream, when
+    given, is the gradient that reaches out_stream beside the norm.  dblock and dresidual may be
+    row inputs.  workspace: norm_gate_backward_workspace(block_out), allocated here when None."""
+    x = block_out
+    rows, n, dt, dev = _train_rows(x, "block_out")
+    if x.requires_grad:
+        _no_history(x, "block_out")
+    _fits(dnormed, "dnormed", x.dtype, x.shape, dev)
+    _fits(out_stream, "out_stream", x.dtype, x.shape, dev)
+    _fits(gamma_post, "gamma_post", x.dtype, (n,), dev)
+    _fits(gamma_pre, "gamma_pre", x.dtype, (n,), dev)
+    pg, kg = _factor(gate, "gate", x, n, dev, True)
+    ps, ks = _factor(res_scale, "res_scale", x, n, dev, False)
+    if dstream is not None:
+        _fits(dstream, "dstream", x.dtype, x.shape, dev)
+    if residual is not None:
+        _fits(residual, "residual", x.dtype, x.shape, dev)
+    dblock = _row_output(dblock, "dblock", x, dev)
+    dresidual = _row_output(dresidual, "dresidual", x, dev)
+    dgamma_post = _weight_gradient(dgamma_post, "dgamma_post", n, x, dev)
+    dgamma_pre = _weight_gradient(dgamma_pre, "dgamma_pre", n, x, dev)
+    if gate is not None:
+        dgate = _factor_gradient(dgate, "dgate", gate, dev)
+    elif dgate is not None:
+        raise ValueError("dgate is given without a gate")
+    if res_scale is not None and residual is not None:
+        dres_scale = _factor_gradient(dres_scale, "dres_scale", res_scale, dev)
+    elif dres_scale is not None:
+        raise ValueError("dres_scale is given without res_scale and residual")
+    ws = norm_gate_backward_workspace(x) if workspace is None else _workspace(workspace, x, dev)
+    _run("mrn_norm_gate_residual_norm_backward", dev, lib().mrn_norm_gate_residual_norm_backward,
+         dnormed.data_ptr(), 0 if dstream is None else dstream.data_ptr(), x.data_ptr(),
+         out_stream.data_ptr(), 0 if residual is None else residual.data_ptr(),
+         gamma_post.data_ptr(), gamma_pre.data_ptr(), pg, kg, ps, ks, dblock.data_ptr(),
+         dresidual.data_ptr(), dgamma_post.data_ptr(), dgamma_pre.data_ptr(),
+         0 if dgate is None else dgate.data_ptr(),
+         0 if dres_scale is None else dres_scale.data_ptr(), ws.data_ptr(), ws.numel(), rows, n,
+         eps_post, eps_pre, dt)
+    _written(tuple(t for t in (dblock, dresidual, dgamma_post, dgamma_pre, dgate, dres_scale)
+                   if t is not None))
+    return dblock, dresidual, dgamma_post, dgamma_pre, dgate, dres_scale
+
+
+# ---------------------------------------------------------------------------
+# The global norm of many tensors, and clipping
+# ---------------------------------------------------------------------------
+def _tensor_list(tensors, name, dev=None):
+    """(ctypes addresses, counts, dtype codes, device index) of a list of contiguous CUDA tensors
+    of float32 or bfloat16."""
+    if _torch is None:
+        _load_torch()
+    f32, bf16 = _torch.float32, _torch.bfloat16
+    codes = []
+    for i, t in enumerate(tensors):
+        dtype = t.dtype
+        codes.append(MRN_F32 if dtype == f32 else MRN_BF16 if dtype == bf16 else _dtype_code(t))
+        at = t.get_device()
+        if dev is None:
+            dev = at
+        if at != dev or at < 0 or not t.is_contiguous():
+            _check(t, f"{name}[{i}]", dtype)
+            raise ValueError(f"{name}[{i}] is on {t.device}, expected cuda:{dev}")
+        if t.requires_grad:
+            _no_history(t, f"{name}[{i}]")
+    n = len(codes)
+    return (_vp * n)(*[t.data_ptr() for t in tensors]), \
+        (_i64 * n)(*[t.numel() for t in tensors]), (_i * n)(*codes), dev
+
+
+def _one_float(t, name, dev):
+    if t is None:
+        return _torch.empty((), dtype=_torch.float32, device=f"cuda:{dev}")
+    if t.numel() != 1:
+        raise ValueError(f"{name} has {t.numel()} elements, expected one")
+    _fits(t, name, _torch.float32, t.shape, dev)
+    return t
+
+
+def _list_workspace(workspace, tensors, dev):
+    if workspace is None:
+        with _torch.cuda.device(dev):
+            return _torch.empty(mrn_grad_norm_workspace(tensors), dtype=_torch.uint8, device="cuda")
+    if workspace.dtype != _torch.uint8 or workspace.get_device() != dev or \
+            not workspace.is_contiguous():
+        _check(workspace, "workspace", _torch.uint8)
+        raise ValueError(f"workspace is on {workspace.device}, expected cuda:{dev}")
+    return workspace
+
+
+def grad_norm_workspace(grads):
+    """Workspace (uint8 tensor) for grad_norm and clip_grad_norm over lists of up to this many
+    tensors, on the first one's device.  Reusable by later calls on one stream; calls that may run
+    at the same time need one each."""
+    *_, dev = _tensor_list(grads[:1], "grads")
+    if dev is None:
+        raise ValueError("grads is empty")
+    return _list_workspace(None, len(grads), dev)
+
+
+def grad_norm(grads, out=None, workspace=None):
+    """The norm of all elements of a sequence of tensors (float32 and bfloat16, mixed as they come;
+    at least one), a float32 tensor of one element on their device.  workspace:
+    grad_norm_workspace(grads), allocated here when None."""
+    pointers, counts, codes, dev = _tensor_list(grads, "grads")
+    if dev is None:
+        raise ValueError("grads is empty")
+    out = _one_float(out, "out", dev)
+    ws = _list_workspace(workspace, len(codes), dev)
+    _run("mrn_grad_norm", dev, lib().mrn_grad_norm, pointers, counts, codes, len(codes),
+         out.data_ptr(), ws.data_ptr(), ws.numel())
+    _written((out,))
+    return out
+
+
+def clip_grad_norm(grads, max_norm: float, out=None, norm=None, workspace=None):
+    """(norm, out): the norm of all elements of grads before clipping, and every tensor times
+    min(1, max_norm / norm); a norm that is not finite leaves the values as they are.  out: a
+    sequence of tensors of the same shapes and types, which may be those of grads; None clips
+    grads in place and returns it.  Nothing is synchronised."""
+    pointers, counts, codes, dev = _tensor_list(grads, "grads")
+    if dev is None:
+        raise ValueError("grads is empty")
+    if out is None:
+        out, outs = grads, pointers
+    else:
+        if len(out) != len(grads):
+            raise ValueError(f"out has {len(out)} tensors, expected {len(grads)}")
+        for i, (o, g) in enumerate(zip(out, grads)):
+            if o.dtype != g.dtype or o.shape != g.shape:
+                _check(o, f"out[{i}]", g.dtype, g.shape)
+        outs, *_ = _tensor_list(out, "out", dev)
+    norm = _one_float(norm, "norm", dev)
+    ws = _list_workspace(workspace, len(codes), dev)
+    _run("mrn_clip_grad_norm", dev, lib().mrn_clip_grad_norm, pointers, outs, counts, codes,
+         len(codes), max_norm, norm.data_ptr(), ws.data_ptr(), ws.numel())
+    _written((*out, norm))
+    return norm, out

@@ -15,9 +15,12 @@
  *   mrn_add_rmsnorm, mrn_rmsnorm_then_add_scale, mrn_rmsnorm_q8_1 (Hesper
  *   "RMSNorm Layer" kernels) and the split-norm seam mrn_rmsnorm_seam,
  *   mrn_rmsnorm_unweighted, mrn_seam_scale ("Chapter 12", section 12.7).
+ * The sandwich tail with a gate on the block and a scale on the residual:
+ *   mrn_norm_gate_residual_norm.
  * For training: mrn_layernorm, mrn_dropout_add, mrn_dropout_add_layernorm and the
  *   gradients mrn_layernorm_backward, mrn_dropout_add_layernorm_backward,
- *   mrn_rmsnorm_backward.
+ *   mrn_rmsnorm_backward, mrn_norm_gate_residual_norm_backward; and the global norm
+ *   of all gradients, mrn_grad_norm, with clipping, mrn_clip_grad_norm.
  *
  * Sources: "Chapter 12 -- RMSNorm and the dual-epsilon sandwich" section 12.1
  * (definition), 12.2 (two epsilons: 1e-8 for the post norms, 1e-5 for the pre
@@ -94,10 +97,13 @@ typedef enum mrn_dtype {
 typedef enum mrn_status {
     MRN_OK = 0,
     MRN_ERR_NULL_POINTER = 1,      /* a required pointer is NULL (rows > 0) */
-    MRN_ERR_INVALID_SIZE = 2,      /* n < 1, rows < 0, rows*n*size overflows, or a
-                                      workspace smaller than the call needs */
-    MRN_ERR_INVALID_EPS = 3,       /* eps not finite or not > 0, or a dropout
-                                      probability outside 0 .. 1 */
+    MRN_ERR_INVALID_SIZE = 2,      /* n < 1, rows < 0, rows*n*size overflows, a
+                                      workspace smaller than the call needs, a number
+                                      of tensors or elements < 0, or a factor of no
+                                      known kind */
+    MRN_ERR_INVALID_EPS = 3,       /* eps not finite or not > 0, a dropout
+                                      probability outside 0 .. 1, or a largest norm
+                                      that is not >= 0 */
     MRN_ERR_UNSUPPORTED_DTYPE = 4, /* dtype not MRN_F32 / MRN_BF16 (seam format not
                                       MRN_F16 / MRN_BF16) */
     MRN_ERR_ALIASING = 5,          /* a forbidden overlap between buffers */
@@ -234,6 +240,47 @@ mrn_status mrn_rmsnorm_unweighted(const void *x, void *u, int64_t rows, int64_t 
                                   mrn_dtype dtype, mrn_dtype seam, cudaStream_t stream);
 mrn_status mrn_seam_scale(const void *u, const void *gamma, void *y, int64_t rows, int64_t n,
                           mrn_dtype seam, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* The dual-epsilon sandwich tail with a gate on the block and a scale on the
+ * residual.  Not on the pages, whose blocks have neither.                     */
+
+/* How the values of a factor are shared by the elements of [rows x n]. */
+typedef enum mrn_factor {
+    MRN_FACTOR_NONE = 0,     /* the factor is one; its pointer is not read */
+    MRN_FACTOR_SCALAR = 1,   /* one value */
+    MRN_FACTOR_CHANNEL = 2,  /* [n]: one per channel, shared by all rows */
+    MRN_FACTOR_ROW = 3       /* [rows]: one per row (the gate only) */
+} mrn_factor;
+
+/*
+ * The tail in one kernel:
+ *   out_stream[r,j] = res_scale * residual[r,j]
+ *                     + gate * gamma_post[j] * block_out[r,j] * inv(block_out[r,:]; eps_post)
+ *   normed[r,j]     = out_stream[r,j] * inv(out_stream[r,:]; eps_pre) * gamma_pre[j]
+ *   block_out   [rows x n]  sub-block output
+ *   residual    [rows x n]  residual stream before the update
+ *   gamma_post  [n]         the post norm's gain
+ *   gamma_pre   [n]         the next pre norm's gain
+ *   gate                    the block's gate, gate_kind any mrn_factor
+ *   res_scale               the residual's scale; MRN_FACTOR_ROW is MRN_ERR_INVALID_SIZE
+ *   out_stream  [rows x n]  may be block_out or residual (in place)
+ *   normed      [rows x n]  may be block_out or residual, never overlapping out_stream
+ * Factors are device memory of `dtype`, read when the kernel runs, so that a captured
+ * graph takes the values of its replay; of a bf16 gate per row the four bytes that hold
+ * a value are read.  Factors are multiplied as they are: a gate of zero does not hide an
+ * infinity or NaN of the block.  The two factors of a channel (gate and gamma_post) are
+ * multiplied first, in f32; bf16: out_stream is rounded once and normed is computed from
+ * the rounded values, as in mrn_norm_residual_norm.
+ * Speed, alignment and geometry: as of the training operations below.
+ */
+mrn_status mrn_norm_gate_residual_norm(const void *block_out, const void *residual,
+                                       const void *gamma_post, const void *gamma_pre,
+                                       const void *gate, mrn_factor gate_kind,
+                                       const void *res_scale, mrn_factor res_scale_kind,
+                                       void *out_stream, void *normed,
+                                       int64_t rows, int64_t n, float eps_post, float eps_pre,
+                                       mrn_dtype dtype, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Training: LayerNorm, dropout before the residual add, and the gradients of
@@ -374,6 +421,87 @@ mrn_status mrn_rmsnorm_backward(const void *dy, const void *x, const void *gamma
                                 void *workspace, int64_t workspace_bytes,
                                 int64_t rows, int64_t n, float eps,
                                 mrn_dtype dtype, cudaStream_t stream);
+
+/*
+ * Bytes of the workspace of mrn_norm_gate_residual_norm_backward for rows x n (either
+ * dtype, any factors) on the current device; as mrn_norm_backward_workspace otherwise.
+ */
+mrn_status mrn_norm_gate_backward_workspace(int64_t rows, int64_t n, int64_t *bytes);
+
+/*
+ * Gradient of mrn_norm_gate_residual_norm (with no factors: of mrn_norm_residual_norm),
+ * from its operands and its out_stream; no statistics are kept, both inv are taken again.
+ * With i = inv(out_stream; eps_pre), w = dnormed * gamma_pre, xh = block_out *
+ * inv(block_out; eps_post):
+ *   ds          = i * (w - out_stream * i^2 * sum_j (w * out_stream) / n) + dstream
+ *   u           = ds * gate * gamma_post
+ *   dblock      = inv(block_out; eps_post) * (u - xh * sum_j (u * xh) / n)
+ *   dresidual   = res_scale * ds
+ *   dgamma_pre  = sum_r dnormed * out_stream * i,   dgamma_post = sum_r ds * gate * xh
+ *   dgate       = ds * gamma_post * xh  summed over the elements that share a gate
+ *   dres_scale  = ds * residual         summed over the elements that share a scale
+ * dblock and dresidual come from the f32 ds, each rounded once.
+ *   dnormed     [rows x n]  gradient of normed
+ *   dstream     [rows x n]  or NULL: the gradient that reaches out_stream beside the norm
+ *   residual    [rows x n]  the forward's; read only when dres_scale is asked for (else
+ *                           it may be NULL), and then not a stream updated in place
+ *   dblock, dresidual  [rows x n]  each may be one of the row inputs, not each other
+ *   dgamma_post, dgamma_pre  [n]  f32
+ *   dgate, dres_scale  f32, as many values as the factor has; NULL: not computed.  With
+ *                           MRN_FACTOR_NONE they must be NULL (else
+ *                           MRN_ERR_NULL_POINTER: the factor is missing).
+ * The same call gives the same bits.  rows == 0 writes zeros to the gradients of weights
+ * and of factors; the other pointers are not read.
+ */
+mrn_status mrn_norm_gate_residual_norm_backward(
+    const void *dnormed, const void *dstream, const void *block_out, const void *out_stream,
+    const void *residual, const void *gamma_post, const void *gamma_pre, const void *gate,
+    mrn_factor gate_kind, const void *res_scale, mrn_factor res_scale_kind, void *dblock,
+    void *dresidual, float *dgamma_post, float *dgamma_pre, float *dgate, float *dres_scale,
+    void *workspace, int64_t workspace_bytes, int64_t rows, int64_t n, float eps_post,
+    float eps_pre, mrn_dtype dtype, cudaStream_t stream);
+
+/*
+ * Bytes of the workspace of mrn_grad_norm and mrn_clip_grad_norm for lists of up to
+ * `tensors` tensors on the current device: scratch, 8-byte aligned device memory, a
+ * workspace each for calls that may run at the same time.
+ */
+mrn_status mrn_grad_norm_workspace(int64_t tensors, int64_t *bytes);
+
+/*
+ * The norm of all elements of a list of tensors:  norm = sqrt(sum_t sum_e grads[t][e]^2)
+ *   grads, counts, dtypes  host arrays of `tensors` entries, read by the call itself (a
+ *           captured graph keeps the entries, not the arrays): the address of a tensor in
+ *           device memory, its number of elements (0: the address is not read) and its
+ *           type, MRN_F32 or MRN_BF16, mixed as they come
+ *   norm    one f32 in device memory; 0 for an empty list
+ * Sums over blocks of elements in f32, over the blocks in 64 bits, in a fixed order: the
+ * same call gives the same bits.  Squares that leave f32's range are taken scaled, so that
+ * norm is right wherever it is an f32 number itself; infinities give infinity, NaN gives
+ * NaN.  A tensor that is listed twice counts twice.
+ * Launches: one kernel per 1024 tensors, and one.
+ */
+mrn_status mrn_grad_norm(const void *const *grads, const int64_t *counts, const mrn_dtype *dtypes,
+                         int64_t tensors, float *norm, void *workspace, int64_t workspace_bytes,
+                         cudaStream_t stream);
+
+/*
+ * The norm as above, and the tensors scaled to a norm of max_norm at most:
+ *   out[t][e] = grads[t][e] * (norm > max_norm ? max_norm / norm : 1)
+ * (the factor rounded once to f32, each product once to the tensor's type).  A norm that is
+ * not finite leaves the values as they are: the caller reads it and skips the step.
+ *   out       host array of addresses; out[t] may be grads[t] itself (in place; nothing is
+ *             written when the factor is one), and must not overlap any other entry of
+ *             grads or out, norm or the workspace
+ *   max_norm  >= 0; infinity: nothing is scaled
+ * Tensors whose two addresses share an offset from a multiple of 32 bytes (16 of bf16) are
+ * moved in whole vectors, others element by element.
+ * Launches: two kernels per 1024 tensors, and one.
+ */
+mrn_status mrn_clip_grad_norm(const void *const *grads, void *const *out, const int64_t *counts,
+                              const mrn_dtype *dtypes, int64_t tensors, double max_norm,
+                              float *norm, void *workspace, int64_t workspace_bytes,
+                              cudaStream_t stream);
 
 /* Static, human-readable name of a status code; never NULL. */
 const char *mrn_status_string(mrn_status status);
