@@ -25,7 +25,8 @@ SOURCES = ["mrn_api.cpp", "mrn_ops_rmsnorm.cu", "mrn_ops_then_add.cu", "mrn_ops_
            "mrn_ops_add_rmsnorm.cu", "mrn_ops_then_add_scale.cu", "mrn_ops_rmsnorm_q8_1.cu",
            "mrn_ops_seam_f16.cu", "mrn_ops_seam_bf16.cu", "mrn_seam_scale.cu",
            "mrn_train_api.cpp", "mrn_layernorm.cu", "mrn_norm_backward.cu", "mrn_dropout.cu",
-           "mrn_gate_api.cpp", "mrn_gate_forward.cu", "mrn_gate_backward.cu", "mrn_grad_norm.cu"]
+           "mrn_gate_api.cpp", "mrn_gate_forward.cu", "mrn_gate_backward_f32.cu",
+           "mrn_gate_backward_bf16.cu", "mrn_grad_norm.cu"]
 
 
 def nvcc() -> str:

@@ -22,6 +22,7 @@
 
 #include "mrn_checks.h"
 #include "mrn_internal.h"
+#include "mrn_gate.h"
 #include "mrn_train.h"
 
 namespace {
@@ -970,7 +971,10 @@ int mrn_wait_timeouts(void) {
                           mrn::take_wait_timeouts_seam_f16(),
                           mrn::take_wait_timeouts_seam_bf16(),
                           mrn::take_wait_timeouts_layernorm(),
-                          mrn::take_wait_timeouts_norm_backward()};
+                          mrn::take_wait_timeouts_norm_backward(),
+                          mrn::take_wait_timeouts_gate(),
+                          mrn::take_wait_timeouts_gate_backward_f32(),
+                          mrn::take_wait_timeouts_gate_backward_bf16()};
     int total = 0;
     for (int v : counts) {
         if (v < 0) {

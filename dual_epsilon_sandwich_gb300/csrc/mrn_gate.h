@@ -1,6 +1,6 @@
 // mrn_gate.h -- host-side interface between the C entry points of the gated
 // sandwich tail and of the operations over many tensors (mrn_gate_api.cpp) and
-// their kernels (mrn_gate_forward.cu, mrn_gate_backward.cu, mrn_grad_norm.cu).
+// their kernels (mrn_gate_forward.cu, mrn_gate_backward.cuh, mrn_grad_norm.cu).
 // Not part of the public ABI.
 #pragma once
 
@@ -39,7 +39,7 @@ struct GateBackwardArgs {
     void *db, *dres;
     float *dg1, *dg2;
     float *dgate, *dscale;  // NULL: not due
-    float *workspace;       // see gate_backward_workspace_floats
+    float *workspace;       // see kGateColumnSets
     int64_t rows, n;
     float eps1, eps2;
     uint32_t stall;
@@ -47,12 +47,22 @@ struct GateBackwardArgs {
 
 cudaError_t launch_gate(bool bf16, const GateArgs &a, int sms, bool pdl, cudaStream_t stream,
                         uint64_t *launches);
-cudaError_t launch_gate_backward(bool bf16, const GateBackwardArgs &a, int sms, bool pdl,
-                                 cudaStream_t stream, uint64_t *launches);
+cudaError_t launch_gate_backward_f32(const GateBackwardArgs &a, int sms, bool pdl, cudaStream_t stream,
+                                     uint64_t *launches);
+cudaError_t launch_gate_backward_bf16(const GateBackwardArgs &a, int sms, bool pdl, cudaStream_t stream,
+                                      uint64_t *launches);
+
+// Bounded waits of these kernels' clusters that ran out since the last call.
+enum { kOpGateTimeouts = 102, kOpGateBackwardF32Timeouts = 103, kOpGateBackwardBF16Timeouts = 104 };
+int take_wait_timeouts_gate();
+int take_wait_timeouts_gate_backward_f32();
+int take_wait_timeouts_gate_backward_bf16();
 
 // Workspace of the tail's gradient: three sets of partial rows (as of the norms' gradients),
-// and behind them the partial sums of the two scalar factors.
+// and behind them, for either scalar factor, one f64 partial sum per CTA, of which a partial row
+// has kGateScalars at most (a cluster's).
 constexpr int64_t kGateColumnSets = 3;
+constexpr int64_t kGateScalars = 16;
 
 // ---------------------------------------------------------------------------
 // Many tensors

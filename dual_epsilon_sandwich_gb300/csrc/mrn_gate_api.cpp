@@ -31,15 +31,14 @@ Factor factor_of(const void *p, mrn_factor kind) {
     return Factor{kind == MRN_FACTOR_NONE ? nullptr : p, kind};
 }
 
-// Workspace of the gated tail's gradient: the sets of partial rows, then for either scalar
-// factor one partial sum per CTA, at most kMaxGateCtas to a partial row.
-constexpr int64_t kMaxGateCtas = 16;
+// Workspace of the gated tail's gradient (see mrn_gate.h).
 mrn_status gate_workspace_bytes(int64_t rows, int64_t n, int64_t *bytes) {
     if (n < 1 || rows < 0 || n > INT64_MAX / 16) return MRN_ERR_INVALID_SIZE;
     const int64_t parts = backward_parts(rows, n, sm_count_of_current_device());
     const int64_t stride = part_stride_of(n);
     if (parts > 0 && stride > INT64_MAX / 32 / parts) return MRN_ERR_INVALID_SIZE;
-    *bytes = (kGateColumnSets * parts * stride + 2 * kMaxGateCtas * parts) * static_cast<int64_t>(sizeof(float));
+    *bytes = kGateColumnSets * parts * stride * static_cast<int64_t>(sizeof(float)) +
+             2 * kGateScalars * parts * static_cast<int64_t>(sizeof(double));
     return MRN_OK;
 }
 
@@ -222,8 +221,8 @@ mrn_status mrn_norm_gate_residual_norm_backward(
     if (workspace_bytes < needed) return MRN_ERR_INVALID_SIZE;
     a.stall = launch_stall_bytes();
     uint64_t launched = 0;
-    const cudaError_t err = launch_gate_backward(dtype == MRN_BF16, a, sm_count_of_current_device(),
-                                                 launch_pdl(), stream, &launched);
+    const auto launch = dtype == MRN_BF16 ? launch_gate_backward_bf16 : launch_gate_backward_f32;
+    const cudaError_t err = launch(a, sm_count_of_current_device(), launch_pdl(), stream, &launched);
     return launch_result(err, launched);
 }
 

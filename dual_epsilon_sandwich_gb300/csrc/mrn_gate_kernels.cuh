@@ -65,4 +65,84 @@ __device__ __forceinline__ void cta_sum(float (&v)[6], CtaSumSix &s, int &turn) 
     for (int i = 0; i < 6; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, t, 4 * i);
 }
 
+template <> struct CtaSumOf<6, false> { using Slots = CtaSumSix; };
+
+// row_sum of six values, with fewer shuffles behind a cluster's messages.
+template <bool WARP>
+__device__ __forceinline__ bool row_sum_six(float (&v)[6], RowSumSlots<6, false> &s, int &turn, int width,
+                                            unsigned cl, unsigned crank, uint32_t stall) {
+    if constexpr (WARP) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) v[i] = group_allsum(v[i], width);
+    } else {
+        cta_sum(v, s.cta, turn);
+        if (cl > 1) {
+            const int p = turn & 1;
+            const unsigned lane = threadIdx.x & 31;
+            if (threadIdx.x == 0) mbar_arrive_expect_tx(&s.bar[p], (cl - 1) * 24u + stall);
+            if (threadIdx.x < cl && threadIdx.x != crank) {
+#pragma unroll
+                for (int i = 0; i < 6; ++i) send_f32(&s.box[p][i][crank], &s.bar[p], threadIdx.x, v[i]);
+            }
+            const bool late = !mbar_wait_bounded_cluster(&s.bar[p], static_cast<uint32_t>((turn - 1) >> 1 & 1));
+            float x[6];
+#pragma unroll
+            for (int i = 0; i < 6; ++i) x[i] = lane >= cl ? 0.0f : (lane == crank ? v[i] : s.box[p][i][lane]);
+            const float t = warp_sum_six(x, static_cast<int>(lane));
+#pragma unroll
+            for (int i = 0; i < 6; ++i)
+                v[i] = __shfl_sync(0xFFFFFFFFu, t, i < 4 ? (i & 1) * 16 + (i >> 1) * 8 : (i & 1) * 16 + 4);
+            if (__syncthreads_or(late)) {
+                if (threadIdx.x == 0) atomicAdd(&g_wait_timeouts, 1u);
+                return false;
+            }
+        }
+    }
+    return true;
+}
+
+// A gate of one value per row travels with its row: one word per lanes that copy together (bf16:
+// the word that holds the element).  A load of it in the loop would hold up every row.
+template <int R, bool EDGE, bool WARP> struct RowGates {
+    static constexpr int kTeams = !WARP ? kCtaWarps : (EDGE ? kWarpTileThreads / kEndLanes : kWarpTileThreads);
+    uint32_t w[kTileMaxStages][R][kTeams];
+};
+template <class T> __device__ __forceinline__ uintptr_t row_gate_at(const Factor &gate, int64_t row) {
+    return reinterpret_cast<uintptr_t>(gate.p) + static_cast<uintptr_t>(row * T::kBytes);
+}
+template <class T> __device__ __forceinline__ void copy_row_gate(uint32_t *to, const Factor &gate, int64_t row) {
+    cp_async4(smem_addr(to), reinterpret_cast<const void *>(row_gate_at<T>(gate, row) & ~uintptr_t(3)));
+}
+template <class T> __device__ __forceinline__ float row_gate(uint32_t w, const Factor &gate, int64_t row) {
+    if constexpr (T::kBytes == 4) return __uint_as_float(w);
+    return __uint_as_float((row_gate_at<T>(gate, row) & 2) ? w & 0xFFFF0000u : w << 16);
+}
+
+// gamma_post of a thread's columns, times the gate of a channel, in f32.
+template <class T, int K, class Tile>
+__device__ __forceinline__ void block_weights(uint64_t (&c)[K][4], const Tile &tile, const void *g1, const Factor &gate) {
+    Slot<T> g[K];
+    tile.weights(g, g1);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[k][i] = g[k].pair(i);
+    if (gate.kind == MRN_FACTOR_CHANNEL) {
+        tile.weights(g, gate.p);
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[k][i] = f2_mul(c[k][i], g[k].pair(i));
+    }
+}
+template <class Tile>
+__device__ __forceinline__ float end_block_weight(const Tile &tile, const void *g1, const Factor &gate) {
+    const float g = tile.end_weight(g1);
+    return gate.kind == MRN_FACTOR_CHANNEL ? g * tile.end_weight(gate.p) : g;
+}
+// A factor that all rows and channels share; one where it is not of that kind.
+template <class T> __device__ __forceinline__ float scalar_factor(const Factor &f) {
+    return f.kind == MRN_FACTOR_SCALAR ? ld_elem<T>(f.p, 0) : 1.0f;
+}
+
 }  // namespace mrn

@@ -70,6 +70,17 @@ __device__ __forceinline__ void ld_shared_slot(Slot<F32> &s, uint32_t p) {
                  : "=r"(s.w[4]), "=r"(s.w[5]), "=r"(s.w[6]), "=r"(s.w[7]) : "r"(p));
 }
 
+__device__ __forceinline__ void st_shared_slot(uint32_t p, const Slot<BF16> &s) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};"
+                 :: "r"(p), "r"(s.w[0]), "r"(s.w[1]), "r"(s.w[2]), "r"(s.w[3]) : "memory");
+}
+__device__ __forceinline__ void st_shared_slot(uint32_t p, const Slot<F32> &s) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};"
+                 :: "r"(p), "r"(s.w[0]), "r"(s.w[1]), "r"(s.w[2]), "r"(s.w[3]) : "memory");
+    asm volatile("st.shared.v4.b32 [%0+16], {%1,%2,%3,%4};"
+                 :: "r"(p), "r"(s.w[4]), "r"(s.w[5]), "r"(s.w[6]), "r"(s.w[7]) : "memory");
+}
+
 // Sums of N values over the threads of a row.  WARP: over `width` lanes; else over
 // the CTA and, for rows split over a cluster, over its CTAs: every CTA sends its sums to
 // every peer as st.async messages, which land in the peer's box for this turn and complete
@@ -315,6 +326,10 @@ template <class T, int K, int R, bool EDGE, bool WARP> struct RowTile {
             }
         }
     }
+    // The same of one slot, not zeroed past the last row.
+    __device__ __forceinline__ void fetch_slot(Slot<T> &s, uint32_t from, int o, int k) const {
+        ld_shared_slot(s, from + o * K * kBlock + slot_from + k * kBlock);
+    }
     // This thread's single element of operand o; 0 when it has none.
     template <class Ends>
     __device__ __forceinline__ float fetch_end(const Ends &end_w, int stage, int o, int rr) const {
@@ -331,6 +346,9 @@ template <class T, int K, int R, bool EDGE, bool WARP> struct RowTile {
 #pragma unroll
         for (int k = 0; k < K; ++k)
             st_slot_if(on && holds(k), p + k * slot_step() * (8 * T::kBytes), s[k]);
+    }
+    __device__ __forceinline__ void store_slot(char *base, bool on, const Slot<T> &s, int k) const {
+        st_slot_if(on && holds(k), base + at + (first + k * slot_step()) * (8 * T::kBytes), s);
     }
     // Stores this thread's single element; returns it as stored.
     __device__ __forceinline__ float store_end(char *base, int rr, bool on, float v) const {
@@ -583,12 +601,13 @@ cudaError_t resident_clusters(TileLaunchCache &cache, void (*fn)(Params...), con
 struct TileGrid {
     int stages;       // 0: the ring does not fit
     int64_t ctas;
-    int64_t shared;   // bytes of the ring
+    int64_t shared;   // bytes of the ring, and of what the kernel keeps beside it
 };
 
 template <class... Params>
 cudaError_t tile_grid(TileLaunchCache &cache, void (*fn)(Params...), const TileShape &s, int64_t rows, int64_t n,
-                      int rows_at_a_time, int elem_bytes, int operands, int most_per_sm, int sms, TileGrid *g) {
+                      int rows_at_a_time, int elem_bytes, int operands, int most_per_sm, int sms, TileGrid *g,
+                      int64_t beside = 0) {
     *g = TileGrid{};
     int per_sm = 0;
     cudaError_t err = open_tile(cache, fn, s.threads, &per_sm);
@@ -596,13 +615,13 @@ cudaError_t tile_grid(TileLaunchCache &cache, void (*fn)(Params...), const TileS
     if (per_sm > most_per_sm) per_sm = most_per_sm;
     const int64_t stage = tile_ring_bytes(elem_bytes, s.k, s.threads, 1, operands * rows_at_a_time);
     for (;; --per_sm) {
-        const int64_t budget = (kTileSharedBudget - (per_sm - 1) * kTileStaticShared) / per_sm;
-        g->stages = static_cast<int>(budget / stage);
+        const int64_t budget = (kTileSharedBudget - (per_sm - 1) * kTileStaticShared) / per_sm - beside;
+        g->stages = budget < 0 ? 0 : static_cast<int>(budget / stage);
         if (g->stages >= 2 || per_sm == 1) break;
     }
     if (g->stages > kTileMaxStages) g->stages = kTileMaxStages;
     if (g->stages < 1) return cudaSuccess;
-    g->shared = stage * g->stages;
+    g->shared = stage * g->stages + beside;
     int64_t groups = static_cast<int64_t>(sms) * per_sm;      // CTAs or clusters
     if (s.cluster > 1) {
         int clusters = 0;

@@ -2,6 +2,7 @@
 import os
 import subprocess
 import sys
+import time
 
 import numpy as np
 import pytest
@@ -512,3 +513,29 @@ def test_past_32_bits():
                              f64(gate[-last:]), f64(scale), None, E1, E2, None)
     for k, v in (("dblock", got[0]), ("dresidual", got[1]), ("dgate", got[4])):
         ref.check(f64(v[-last:]), *want[k], "f32" if k == "dgate" else "bf16", k)
+def test_a_cluster_whose_messages_are_late_stops_and_recovers():
+    """The test hook lets the first wait of a cluster expect bytes that never come: the calls
+    return, mrn_wait_timeouts() reports them, and the next calls are exact."""
+    rows, n = 3, 16384
+    b, res, g1, g2 = operands(90, rows, n, "f32")
+    s, dn = make(91, rows, n, "f32"), make(92, rows, n, "f32")
+    v = [t.cuda() for t in (b, res, g1, g2, s, dn)]
+    mrn.mrn_wait_timeouts()
+    torch.cuda.synchronize()
+    assert mrn.mrn_set_launch_options(mrn.MRN_LAUNCH_PDL | mrn.MRN_LAUNCH_TEST_WAIT_TIMEOUT) == 0
+    try:
+        t0 = time.perf_counter()
+        mrn.norm_gate_residual_norm(*v[:4])
+        mrn.norm_gate_residual_norm_backward(v[5], v[0], v[4], v[2], v[3])
+        torch.cuda.synchronize()
+        seconds = time.perf_counter() - t0
+    finally:
+        mrn.mrn_set_launch_options(mrn.MRN_LAUNCH_PDL)
+    assert mrn.mrn_wait_timeouts() >= 2 and seconds < 30, seconds
+    check_forward(run_forward(b, res, g1, g2, None, None, "f32"), b, res, g1, g2, None, None, "f32",
+                  "after a timeout")
+    got = run_backward(dn, b, s, g1, g2, None, None, None, None, "f32")
+    check_backward(got, dn, b, s, g1, g2, None, None, None, None, "f32", "after a timeout")
+    assert mrn.mrn_wait_timeouts() == 0
+
+
