@@ -479,7 +479,7 @@ mrn_status mrn_grad_norm_workspace(int64_t tensors, int64_t *bytes);
  * same call gives the same bits.  Squares that leave f32's range are taken scaled, so that
  * norm is right wherever it is an f32 number itself; infinities give infinity, NaN gives
  * NaN.  A tensor that is listed twice counts twice.
- * Launches: one kernel per 1024 tensors, and one.
+ * Launches: one kernel per 960 tensors, and one.
  */
 mrn_status mrn_grad_norm(const void *const *grads, const int64_t *counts, const mrn_dtype *dtypes,
                          int64_t tensors, float *norm, void *workspace, int64_t workspace_bytes,
@@ -496,7 +496,7 @@ mrn_status mrn_grad_norm(const void *const *grads, const int64_t *counts, const 
  *   max_norm  >= 0; infinity: nothing is scaled
  * Tensors whose two addresses share an offset from a multiple of 32 bytes (16 of bf16) are
  * moved in whole vectors, others element by element.
- * Launches: two kernels per 1024 tensors, and one.
+ * Launches: two kernels per 960 tensors (for an empty list, one kernel).
  */
 mrn_status mrn_clip_grad_norm(const void *const *grads, void *const *out, const int64_t *counts,
                               const mrn_dtype *dtypes, int64_t tensors, double max_norm,
