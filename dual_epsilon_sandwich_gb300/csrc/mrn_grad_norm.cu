@@ -12,10 +12,14 @@ namespace mrn {
 
 constexpr int kListThreads = 256;
 constexpr int kListCtasPerSm = 4;
-constexpr int kListFlight = 4;          // slots of a thread in flight
-constexpr int kListStep = kListThreads * kListFlight;
+// Slots of a thread in flight, 128 bytes of either type, and slots of one step of a CTA.
+template <class T> struct ListFlight { static constexpr int kSlots = 16 / T::kBytes; };
+constexpr int kListStepSlots = 8;
+constexpr int kListStep = kListThreads * kListStepSlots;
+constexpr int kListUnit = 2;            // slots of a thread at least
 constexpr int kListTensors = 960;       // per launch: what 32,764 bytes of parameters hold
-constexpr int kListFew = 120;           // ... and a form of less than 4096 bytes
+constexpr int kListFew = 86;            // ... and a form of less than 4096 bytes
+constexpr int kListCtas = 608;          // four for each of 152 SMs
 
 struct ListEntry {
     const void *in;
@@ -29,9 +33,11 @@ struct ListEntry {
 template <int N> struct ListArgs {
     ListEntry t[N];
     int64_t total;             // slots of all tensors
-    int64_t per_cta;           // slots of one CTA, a multiple of kListStep
+    int64_t per_cta;           // slots of one CTA, a multiple of kListThreads
     int tensors;
+    uint16_t start[kListCtas + 1];   // the tensor of a CTA's first slot
 };
+static_assert(sizeof(ListArgs<kListTensors>) <= 32764 - 64 && sizeof(ListArgs<kListFew>) <= 4096 - 64, "kernel parameters");
 
 // Elements from the slot boundary below a tensor to its first.
 MRN_HOST_DEVICE inline int list_offset(const void *p, bool bf16) {
@@ -49,75 +55,122 @@ template <int N> __device__ __forceinline__ int list_find(const ListArgs<N> &l, 
     return lo;
 }
 
-// The sum over the CTA of a value in 64 bits, in a fixed order, for all threads.
+// The sum over the CTA of a value in 64 bits, in a fixed order; valid in the first warp.  (An SM
+// does two 64-bit additions a clock: all warps adding up shuffles took a microsecond per CTA.)
 __device__ __forceinline__ double list_cta_sum(double v) {
-    __shared__ double s[kListThreads / 32];
+    __shared__ double s[kListThreads];
+    s[threadIdx.x] = v;
+    __syncthreads();
+    if (threadIdx.x >= 32) return 0.0;
+#pragma unroll
+    for (int w = 1; w < kListThreads / 32; ++w) v += s[threadIdx.x + 32 * w];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = s[0];
-#pragma unroll
-    for (int w = 1; w < kListThreads / 32; ++w) v += s[w];
     return v;
 }
 
-// The squares of a thread's slots, in f32: two chains of at most 16 additions.
-template <class T> __device__ __forceinline__ float slot_squares(const Slot<T> (&s)[kListFlight]) {
-    uint64_t acc = 0;
-#pragma unroll
-    for (int u = 0; u < kListFlight; ++u)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc = f2_fma(s[u].pair(i), s[u].pair(i), acc);
-    return f2_sum(acc);
-}
-// The same where f32 has lost squares, in 64 bits.  Below 2^-100 those under f32's normal range may
-// have been a share of the sum; at the other end it is infinite.  (Zeros are left out: gradients
-// hold whole blocks of them, and 64-bit arithmetic is slow.)
-template <class T> __device__ __noinline__ double slot_squares_f64(const Slot<T> (&s)[kListFlight]) {
-    uint32_t any = 0;
-#pragma unroll
-    for (int u = 0; u < kListFlight; ++u)
-#pragma unroll
-        for (int w = 0; w < Slot<T>::kWords; ++w) any |= s[u].w[w] << (T::kBytes == 4 ? 1 : 0);
+// Squares in f32 are kept where none can have been lost: below 2^-100 those under f32's normal
+// range may have been a share of the sum; at the other end it is infinite.
+__device__ __forceinline__ bool squares_hold(float q) { return q >= 0x1p-100f && q < INFINITY; }
+
+// The squares of `slots` whole slots, a CTA's width apart, in 64 bits.  (Zeros are left out:
+// gradients hold whole blocks of them, and 64-bit arithmetic is slow.)
+template <class T> __device__ __forceinline__ double list_squares_f64(const void *in, int64_t at, int slots) {
     double sum = 0.0;
-    if (T::kBytes == 2) any &= 0x7FFF7FFFu;
-    if (any == 0) return sum;
+#pragma unroll 1
+    for (int u = 0; u < slots; ++u) {
+        Slot<T> s;
+        ld_slot(s, elem_ptr<T>(in, at + u * (kListThreads * 8)));
+        uint32_t any = 0;
 #pragma unroll
-    for (int u = 0; u < kListFlight; ++u)
+        for (int w = 0; w < Slot<T>::kWords; ++w) any |= s.w[w] & (T::kBytes == 4 ? 0x7FFFFFFFu : 0x7FFF7FFFu);
+        if (any == 0) continue;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum += static_cast<double>(s[u].get(i)) * s[u].get(i);
+        for (int i = 0; i < 8; ++i) sum += static_cast<double>(s.get(i)) * s.get(i);
+    }
     return sum;
 }
-template <class T> __device__ __forceinline__ double squares_of(const Slot<T> (&s)[kListFlight]) {
-    const float q = slot_squares(s);
-    return q >= 0x1p-100f && q < INFINITY ? static_cast<double>(q) : slot_squares_f64(s);
+
+// The squares of a thread's share of a step: in f32 two chains of at most 32 additions.
+template <class T> __device__ __forceinline__ double list_squares_whole(const void *in, int64_t at) {
+    constexpr int F = ListFlight<T>::kSlots;
+    double sum = 0.0;
+#pragma unroll
+    for (int h = 0; h < kListStepSlots; h += F) {
+        Slot<T> s[F];
+#pragma unroll
+        for (int u = 0; u < F; ++u) ld_slot(s[u], elem_ptr<T>(in, at + (h + u) * (kListThreads * 8)));
+        uint64_t acc = 0;
+#pragma unroll
+        for (int u = 0; u < F; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc = f2_fma(s[u].pair(i), s[u].pair(i), acc);
+        const float q = f2_sum(acc);
+        sum += squares_hold(q) ? static_cast<double>(q)
+                               : list_squares_f64<T>(in, at + h * (kListThreads * 8), F);
+    }
+    return sum;
 }
 
-// A slot that is not whole: its elements one by one, zeros outside the tensor.
-template <class T> __device__ __forceinline__ void list_load(Slot<T> &s, const ListEntry &e, int64_t slot, int offset) {
-    const int64_t j0 = slot * 8 - offset, count = e.elements();
-    if (j0 >= 0 && j0 + 8 <= count) {
-        ld_slot(s, elem_ptr<T>(e.in, j0));
+// Where one slot of a step stands: of the tensor it belongs to, elements j .. j + 8 (cut to its own).
+struct ListPlace {
+    const void *in;
+    void *out;
+    int64_t j, count;
+    bool bf16;
+    __device__ __forceinline__ bool whole() const { return j >= 0 && j + 8 <= count; }
+};
+template <int N>
+__device__ __forceinline__ ListPlace list_place(const ListArgs<N> &l, int64_t s, int first, int last) {
+    const ListEntry &e = l.t[list_find(l, s, first, last)];
+    ListPlace p = {e.in, e.out, 0, e.elements(), e.bf16()};
+    p.j = (s - e.first) * 8 - list_offset(e.in, p.bf16);
+    return p;
+}
+// A slot as raw words, of either type: bf16 fills the first four.
+__device__ __forceinline__ void list_load(Slot<F32> &s, const ListPlace &p) {
+    const char *at = static_cast<const char *>(p.in) + p.j * (p.bf16 ? 2 : 4);
+    if (p.whole()) {
+        if (p.bf16) {
+            Slot<BF16> h;
+            ld_slot(h, at);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s.w[i] = h.w[i];
+        } else {
+            ld_slot(s, at);
+        }
         return;
     }
-    s.zero();
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        if (j0 + i < 0 || j0 + i >= count) continue;
-        Frag<T, 1> f;
-        ld_plain(f, elem_ptr<T>(e.in, j0 + i));
-        if constexpr (T::kBytes == 4) s.w[i] = f.w;
-        else s.w[i >> 1] |= static_cast<uint32_t>(f.h) << ((i & 1) * 16);
+        if (p.j + i < 0 || p.j + i >= p.count) continue;
+        if (p.bf16) {
+            s.w[i >> 1] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(at)[i]) << ((i & 1) * 16);
+        } else {
+            s.w[i] = reinterpret_cast<const uint32_t *>(at)[i];
+        }
     }
 }
-
-template <class T> __device__ __forceinline__ double list_squares_whole(const void *in, int64_t at) {
-    Slot<T> s[kListFlight];
+__device__ __forceinline__ Slot<BF16> list_half(const Slot<F32> &s) {
+    Slot<BF16> h;
 #pragma unroll
-    for (int u = 0; u < kListFlight; ++u) ld_slot(s[u], elem_ptr<T>(in, at + u * (kListThreads * 8)));
-    return squares_of(s);
+    for (int i = 0; i < 4; ++i) h.w[i] = s.w[i];
+    return h;
 }
+template <class T> __device__ __forceinline__ double slot_squares(const Slot<T> &s) {
+    uint64_t acc = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc = f2_fma(s.pair(i), s.pair(i), acc);
+    const float q = f2_sum(acc);
+    if (squares_hold(q)) return static_cast<double>(q);
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (s.get(i) != 0.0f) sum += static_cast<double>(s.get(i)) * s.get(i);
+    return sum;
+}
+
+constexpr int kListMixed = 2;      // slots of a thread in flight where a step meets several tensors
 
 template <int N>
 __global__ void __launch_bounds__(kListThreads, kListCtasPerSm)
@@ -126,33 +179,34 @@ mrn_grad_squares_kernel(const __grid_constant__ ListArgs<N> l, double *parts) {
     const int64_t lo = blockIdx.x * l.per_cta;
     const int64_t hi = lo + l.per_cta < l.total ? lo + l.per_cta : l.total;
     double sum = 0.0;
-    int t = list_find(l, lo, 0, l.tensors - 1);
+    int t = l.start[blockIdx.x];
     for (int64_t base = lo; base < hi; base += kListStep) {
         int last = t;                                   // the tensor of the step's last slot
         const int64_t end = base + kListStep < hi ? base + kListStep : hi;
         if (t + 1 < l.tensors && l.t[t + 1].first < end) last = list_find(l, end - 1, t, l.tensors - 1);
         const ListEntry &e = l.t[t];
-        const int offset = list_offset(e.in, e.bf16());
-        const int64_t at = (base - e.first) * 8 - offset;
+        const int64_t at = (base - e.first) * 8 - list_offset(e.in, e.bf16());
         if (last == t && at >= 0 && at + kListStep * 8 <= e.elements() && base + kListStep <= hi) {
             sum += e.bf16() ? list_squares_whole<BF16>(e.in, at + threadIdx.x * 8)
                             : list_squares_whole<F32>(e.in, at + threadIdx.x * 8);
         } else {
-            // the end of a tensor: each slot finds its own
-            Slot<BF16> h[kListFlight];
-            Slot<F32> f[kListFlight];
+            // a tensor's end, or several tensors: each slot finds its own
+#pragma unroll 1
+            for (int64_t s0 = base + threadIdx.x; s0 < end; s0 += kListMixed * kListThreads) {
+                Slot<F32> s[kListMixed];
+                bool bf16[kListMixed];
 #pragma unroll
-            for (int u = 0; u < kListFlight; ++u) {
-                h[u].zero();
-                f[u].zero();
-                const int64_t s = base + u * kListThreads + threadIdx.x;
-                if (s >= end) continue;
-                const ListEntry &own = l.t[list_find(l, s, t, last)];
-                if (own.bf16()) list_load(h[u], own, s - own.first, list_offset(own.in, true));
-                else list_load(f[u], own, s - own.first, list_offset(own.in, false));
+                for (int u = 0; u < kListMixed; ++u) {
+                    s[u].zero();
+                    bf16[u] = false;
+                    if (s0 + u * kListThreads >= end) continue;
+                    const ListPlace p = list_place(l, s0 + u * kListThreads, t, last);
+                    bf16[u] = p.bf16;
+                    list_load(s[u], p);
+                }
+#pragma unroll
+                for (int u = 0; u < kListMixed; ++u) sum += bf16[u] ? slot_squares(list_half(s[u])) : slot_squares(s[u]);
             }
-            sum += squares_of(h);
-            sum += squares_of(f);
         }
         t = last;
         if (t + 1 < l.tensors && l.t[t + 1].first <= end) ++t;
@@ -161,16 +215,29 @@ mrn_grad_squares_kernel(const __grid_constant__ ListArgs<N> l, double *parts) {
     if (threadIdx.x == 0) parts[blockIdx.x] = sum;
 }
 
-__device__ __forceinline__ double norm_of(const double *parts, int64_t count) {
+// The root of the sum of the partial sums, and its inverse (0 where the norm is zero or not
+// finite); valid in the first warp.  One step of Newton's in 64 bits from rsqrtf of the sum scaled
+// to 1 .. 4 leaves 2^-42 (a 64-bit root and a quotient would take four times as long, in every
+// CTA).
+struct Norm {
+    double norm, inv;
+};
+__device__ __forceinline__ Norm norm_of(const double *parts, int64_t count) {
     double sum = 0.0;
     for (int64_t i = threadIdx.x; i < count; i += kListThreads) sum += parts[i];
-    return sqrt(list_cta_sum(sum));
+    sum = list_cta_sum(sum);
+    if (!(sum > 0.0) || !(sum < INFINITY)) return Norm{sum, 0.0};
+    const int e = ((__double2hiint(sum) >> 20) - 1023) & ~1;
+    const double m = sum * __hiloint2double((1023 - e) << 20, 0);
+    double y = static_cast<double>(rsqrtf(static_cast<float>(m)));
+    y = fma(0.5 * y, fma(-m * y, y, 1.0), y);
+    return Norm{m * y * __hiloint2double((1023 + e / 2) << 20, 0), y * __hiloint2double((1023 - e / 2) << 20, 0)};
 }
 
 __global__ void __launch_bounds__(kListThreads)
 mrn_grad_norm_kernel(const double *parts, int64_t count, float *norm) {
     pdl_enter();
-    const double v = norm_of(parts, count);
+    const double v = norm_of(parts, count).norm;
     if (threadIdx.x == 0) *norm = static_cast<float>(v);
 }
 
@@ -182,33 +249,39 @@ template <class T> __device__ __forceinline__ void slot_scale(Slot<T> &s, uint64
 }
 template <class T>
 __device__ __forceinline__ void list_scale_whole(const void *in, void *out, int64_t at, uint64_t k, bool clip) {
-    Slot<T> s[kListFlight];
+    constexpr int F = ListFlight<T>::kSlots;
 #pragma unroll
-    for (int u = 0; u < kListFlight; ++u) ld_slot(s[u], elem_ptr<T>(in, at + u * (kListThreads * 8)));
+    for (int h = 0; h < kListStepSlots; h += F) {
+        Slot<T> s[F];
 #pragma unroll
-    for (int u = 0; u < kListFlight; ++u) {
-        slot_scale(s[u], k, clip);
-        st_slot(elem_ptr<T>(out, at + u * (kListThreads * 8)), s[u]);
+        for (int u = 0; u < F; ++u) ld_slot(s[u], elem_ptr<T>(in, at + (h + u) * (kListThreads * 8)));
+#pragma unroll
+        for (int u = 0; u < F; ++u) {
+            slot_scale(s[u], k, clip);
+            st_slot(elem_ptr<T>(out, at + (h + u) * (kListThreads * 8)), s[u]);
+        }
     }
 }
-template <class T>
-__device__ __forceinline__ void list_scale_slot(const ListEntry &e, int64_t slot, uint64_t k, bool clip) {
-    const int offset = list_offset(e.in, T::kBytes == 2);
-    Slot<T> s;
-    list_load(s, e, slot, offset);
-    slot_scale(s, k, clip);
-    const int64_t j0 = slot * 8 - offset, count = e.elements();
-    if (j0 >= 0 && j0 + 8 <= count && list_offset(e.out, T::kBytes == 2) == offset) {
-        st_slot(elem_ptr<T>(e.out, j0), s);
+__device__ __forceinline__ void list_store(Slot<F32> &s, const ListPlace &p, uint64_t k, bool clip) {
+    Slot<BF16> h = list_half(s);
+    if (p.bf16) {
+        slot_scale(h, k, clip);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s.w[i] = h.w[i];
+    } else {
+        slot_scale(s, k, clip);
+    }
+    char *at = static_cast<char *>(p.out) + p.j * (p.bf16 ? 2 : 4);
+    if (p.whole() && list_offset(at, p.bf16) == 0) {
+        if (p.bf16) st_slot(at, h);
+        else st_slot(at, s);
         return;
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        if (j0 + i < 0 || j0 + i >= count) continue;
-        Frag<T, 1> f;
-        if constexpr (T::kBytes == 4) f.w = s.w[i];
-        else f.h = static_cast<unsigned short>(s.w[i >> 1] >> ((i & 1) * 16));
-        st_global(elem_ptr<T>(e.out, j0 + i), f);
+        if (p.j + i < 0 || p.j + i >= p.count) continue;
+        if (p.bf16) reinterpret_cast<uint16_t *>(at)[i] = static_cast<uint16_t>(s.w[i >> 1] >> ((i & 1) * 16));
+        else reinterpret_cast<uint32_t *>(at)[i] = s.w[i];
     }
 }
 
@@ -219,35 +292,48 @@ __global__ void __launch_bounds__(kListThreads, kListCtasPerSm)
 mrn_grad_scale_kernel(const __grid_constant__ ListArgs<N> l, const double *parts, int64_t count, double max_norm,
                       float *norm_out) {
     pdl_enter();
-    const double norm = norm_of(parts, count);
-    if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = static_cast<float>(norm);
-    const bool clip = norm > max_norm && isfinite(static_cast<float>(norm));
-    const float kf = clip ? static_cast<float>(max_norm / norm) : 1.0f;
+    __shared__ float factor;
+    const Norm n = norm_of(parts, count);
+    if (threadIdx.x == 0) {
+        const float norm = static_cast<float>(n.norm);
+        if (norm_out && blockIdx.x == 0) *norm_out = norm;
+        factor = n.norm > max_norm && norm < INFINITY ? static_cast<float>(max_norm * n.inv) : 1.0f;
+    }
+    __syncthreads();
+    const float kf = factor;
+    const bool clip = kf != 1.0f;
     const uint64_t k = f2_pack(kf, kf);
     const int64_t lo = blockIdx.x * l.per_cta;
     const int64_t hi = lo + l.per_cta < l.total ? lo + l.per_cta : l.total;
-    int last = list_find(l, hi - 1, 0, l.tensors - 1);
+    int last = l.start[blockIdx.x + 1];                     // the tensor of the stretch's last slot
+    if (l.t[last].first >= hi) --last;
     for (int64_t base = lo + (hi - 1 - lo) / kListStep * kListStep; base >= lo; base -= kListStep) {
         const int64_t end = base + kListStep < hi ? base + kListStep : hi;
         const int t = l.t[last].first <= base ? last : list_find(l, base, 0, last);
         const ListEntry &e = l.t[t];
-        const int offset = list_offset(e.in, e.bf16());
-        const int64_t at = (base - e.first) * 8 - offset;
+        const int64_t at = (base - e.first) * 8 - list_offset(e.in, e.bf16());
         if (t == last && !clip && e.in == e.out) {
             // nothing to write
         } else if (t == last && at >= 0 && at + kListStep * 8 <= e.elements() && base + kListStep <= hi &&
-                   list_offset(e.out, e.bf16()) == offset) {
+                   list_offset(e.out, e.bf16()) == list_offset(e.in, e.bf16())) {
             if (e.bf16()) list_scale_whole<BF16>(e.in, e.out, at + threadIdx.x * 8, k, clip);
             else list_scale_whole<F32>(e.in, e.out, at + threadIdx.x * 8, k, clip);
         } else {
+#pragma unroll 1
+            for (int64_t s0 = base + threadIdx.x; s0 < end; s0 += kListMixed * kListThreads) {
+                Slot<F32> s[kListMixed];
+                ListPlace p[kListMixed];
 #pragma unroll
-            for (int u = 0; u < kListFlight; ++u) {
-                const int64_t s = base + u * kListThreads + threadIdx.x;
-                if (s >= end) continue;
-                const ListEntry &own = l.t[list_find(l, s, t, last)];
-                if (!clip && own.in == own.out) continue;
-                if (own.bf16()) list_scale_slot<BF16>(own, s - own.first, k, clip);
-                else list_scale_slot<F32>(own, s - own.first, k, clip);
+                for (int u = 0; u < kListMixed; ++u) {
+                    s[u].zero();
+                    p[u].in = p[u].out = nullptr;
+                    if (s0 + u * kListThreads >= end) continue;
+                    p[u] = list_place(l, s0 + u * kListThreads, t, last);
+                    list_load(s[u], p[u]);
+                }
+#pragma unroll
+                for (int u = 0; u < kListMixed; ++u)
+                    if (p[u].out && (clip || p[u].in != p[u].out)) list_store(s[u], p[u], k, clip);
             }
         }
         last = t;
@@ -255,9 +341,11 @@ mrn_grad_scale_kernel(const __grid_constant__ ListArgs<N> l, const double *parts
     }
 }
 
+int64_t list_ctas(int sms) { return sms * kListCtasPerSm < kListCtas ? sms * kListCtasPerSm : kListCtas; }
+
 int64_t grad_norm_partials(int64_t tensors, int sms) {
     const int64_t launches = (tensors + kListTensors - 1) / kListTensors;
-    return (launches < 1 ? 1 : launches) * sms * kListCtasPerSm;
+    return (launches < 1 ? 1 : launches) * list_ctas(sms);
 }
 
 // The entries from .. to as one launch's parameters; false when all of them are empty.
@@ -273,9 +361,15 @@ bool fill_list(ListArgs<N> &a, const TensorList &l, int64_t from, int64_t to, in
         a.total += (l.counts[from] + list_offset(l.in[from], bf16) + 7) / 8;
     }
     if (a.tensors == 0) return false;
-    const int64_t most = int64_t(sms) * kListCtasPerSm;
-    a.per_cta = ((a.total + most - 1) / most + kListStep - 1) / kListStep * kListStep;
+    const int64_t most = list_ctas(sms);
+    const int64_t each = (a.total + most - 1) / most, unit = each < kListStep ? kListThreads * kListUnit : kListStep;
+    a.per_cta = (each + unit - 1) / unit * unit;
     *ctas = (a.total + a.per_cta - 1) / a.per_cta;
+    int t = 0;
+    for (int64_t c = 0; c <= *ctas; ++c) {
+        while (t + 1 < a.tensors && a.t[t + 1].first <= c * a.per_cta) ++t;
+        a.start[c] = static_cast<uint16_t>(t);
+    }
     return true;
 }
 
