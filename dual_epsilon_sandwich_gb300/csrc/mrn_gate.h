@@ -61,6 +61,15 @@ int take_wait_timeouts_gate_backward_bf16();
 // Workspace of the tail's gradient: three sets of partial rows (as of the norms' gradients),
 // and behind them, for either scalar factor, one f64 partial sum per CTA, of which a partial row
 // has kGateScalars at most (a cluster's).
+// Partial rows at most: as many as CTAs run at once, twice as many where rows are narrow.
+constexpr int gate_parts_per_sm(int64_t n) { return n <= 2048 ? 8 : 4; }
+inline int64_t gate_parts(int64_t rows, int64_t n, int sms) {
+    int64_t parts = static_cast<int64_t>(sms) * gate_parts_per_sm(n);
+    const int64_t by_size = (int64_t(1) << 27) / n;
+    if (parts > by_size) parts = by_size;
+    if (parts > rows) parts = rows;
+    return parts < 1 ? (rows > 0 ? 1 : 0) : parts;
+}
 constexpr int64_t kGateColumnSets = 3;
 constexpr int64_t kGateScalars = 16;
 

@@ -34,7 +34,7 @@ Factor factor_of(const void *p, mrn_factor kind) {
 // Workspace of the gated tail's gradient (see mrn_gate.h).
 mrn_status gate_workspace_bytes(int64_t rows, int64_t n, int64_t *bytes) {
     if (n < 1 || rows < 0 || n > INT64_MAX / 16) return MRN_ERR_INVALID_SIZE;
-    const int64_t parts = backward_parts(rows, n, sm_count_of_current_device());
+    const int64_t parts = gate_parts(rows, n, sm_count_of_current_device());
     const int64_t stride = part_stride_of(n);
     if (parts > 0 && stride > INT64_MAX / 32 / parts) return MRN_ERR_INVALID_SIZE;
     *bytes = kGateColumnSets * parts * stride * static_cast<int64_t>(sizeof(float)) +

@@ -139,9 +139,9 @@ mrn_gate_backward_looped_kernel(const GateBackwardArgs a, const GateParts parts)
 
 // Threads that an SM's registers are shared between (the launch bound): what a thread with k
 // slots needs.
-template <class T> constexpr int gate_backward_resident(int k, int res) {
-    const int words = k * (8 * (res == 2 ? 4 : 3) + Slot<T>::kWords);
-    return words <= 40 ? 640 : (words <= 56 ? 512 : (words <= 96 ? 384 : 256));
+template <class T> constexpr int gate_backward_resident(int k, int res, bool warp) {
+    const int words = k * (8 * (res == 2 ? 4 : 3) + Slot<T>::kWords) + (warp ? 24 : 0);
+    return words <= 56 ? 512 : (words <= 64 ? 448 : (words <= 108 ? 384 : 256));
 }
 
 // a += v with the rounding's loss kept in b (Knuth's two-sum, "The Art of Computer Programming",
@@ -160,14 +160,14 @@ __device__ __forceinline__ void add_kept(float &a, float &b, float v) {
 //   A scale per channel stands in shared memory behind the ring, each thread's columns where it
 // alone reads them: registers are what bounds the number of warps.
 template <class T, int K, bool EDGE, bool WARP, int RES>
-__global__ void __launch_bounds__(gate_backward_resident<T>(K, RES))
+__global__ void __launch_bounds__(gate_backward_resident<T>(K, RES, WARP))
 mrn_gate_backward_tile_kernel(const GateBackwardArgs a, const TileArgs t, const GateParts parts,
                               const uint32_t ring_total) {
     extern __shared__ __align__(16) unsigned char ring_bytes[];
     constexpr int kOps = RES ? 5 : 4;
     __shared__ RowSumSlots<6, false> slots;
     __shared__ EndSlots<kOps, 1, EDGE, WARP> end_w;
-    __shared__ RowGates<1, EDGE, WARP> gates;
+    __shared__ RowGates<EDGE, WARP> gates;
     __shared__ double last[2][kCtaWarps];
     RowTile<T, K, 1, EDGE, WARP> tile(a.rows, a.n, t);
     const int64_t back = static_cast<int64_t>(t.mis) * T::kBytes;
@@ -187,13 +187,13 @@ mrn_gate_backward_tile_kernel(const GateBackwardArgs a, const TileArgs t, const 
     const uint32_t ring0 = static_cast<uint32_t>(__cvta_generic_to_shared(ring_bytes));
     const uint32_t ring = tile.warp_ring(ring0, t.stages, ops_count);
     const bool by_row = a.gate.kind == MRN_FACTOR_ROW;
-    const bool by_channel = a.scale.kind == MRN_FACTOR_CHANNEL;
+    const bool by_channel = RES == 2 || (RES == 0 && a.scale.kind == MRN_FACTOR_CHANNEL);
     tile.clear(ring, t.stages, ops_count);
     row_sum_setup(slots, tile.cl);
     pdl_enter();
     int64_t gate_row = tile.row;
     auto issue = [&](int to) {
-        if (by_row && tile.leads && tile.copy_left > 0) copy_row_gate<T>(&gates.w[to][0][tile.team], a.gate, gate_row);
+        if (by_row && tile.leads && tile.copy_left > 0) copy_row_gate<T>(&gates.w[to][tile.team], a.gate, gate_row);
         gate_row += tile.stride;
         tile.issue(ring + to * walk.bytes, to, ops, ops_count, end_w);
     };
@@ -281,7 +281,7 @@ mrn_gate_backward_tile_kernel(const GateBackwardArgs a, const TileArgs t, const 
             s[4] = fmaf(e_s, cb, s[4]);
             s[5] = fmaf(e_d, cb, s[5]);
         }
-        const float g = by_row && ok ? row_gate<T>(gates.w[walk.read][0][tile.team], a.gate, tile.row) : gate;
+        const float g = by_row && ok ? row_gate<T>(gates.w[walk.read][tile.team], a.gate, tile.row) : gate;
         if (!row_sum_six<WARP>(s, slots, turn, tile.width, tile.cl, tile.crank, turn == 0 ? t.stall : 0u)) break;
         const RowScalars q = row_scalars(s, inv_n, a.eps1, a.eps2, [](float v) { return inv_sqrt(v); });
         if (a.dgate && by_row && tile.first == 0 && ok) a.dgate[tile.row] = q.q;
@@ -528,7 +528,7 @@ bool launch_gate_backward_tile(const GateBackwardArgs &a, const GateParts &parts
     const int64_t alpha = a.scale.kind == MRN_FACTOR_CHANNEL ? int64_t(K) * p.threads * 8 * T::kBytes : 0;
     TileGrid g;
     // (WARP: the epilogue's rows have room for the ends)
-    l.err = tile_grid(cache, fn, p, a.rows, a.n, 1, T::kBytes, operands, 4, l.sms, &g, alpha + (WARP ? 1024 : 0));
+    l.err = tile_grid(cache, fn, p, a.rows, a.n, 1, T::kBytes, operands, gate_parts_per_sm(a.n), l.sms, &g, alpha + (WARP ? 1024 : 0));
     if (l.err != cudaSuccess) return true;
     l.parts = g.ctas / p.cluster;
     l.ctas = g.ctas;
@@ -552,10 +552,25 @@ bool launch_gate_backward_k(const GateBackwardArgs &a, const GateParts &parts, c
                       : launch_gate_backward_tile<T, K, false, WARP, 2>(a, parts, p, l);
 }
 
+// Slots per thread (k) for rows of a CTA, and threads of one at most.
+template <class T> void gate_backward_tile(int64_t slots, bool edge, bool residual, bool columns, int *k, int *threads) {
+    if (T::kBytes == 2) {
+        if (columns) *k = slots <= 384 ? 2 : 4;
+        else *k = slots > 640 ? 4 : (slots <= 400 || edge ? 3 : 2);
+    } else if (residual) {
+        *k = slots <= 560 ? 2 : 1;
+    } else {
+        *k = slots <= 160 ? 1 : (slots <= 384 ? 4 : (slots <= 560 ? 3 : (slots <= 700 ? 4 : (slots <= 896 ? 2 : 4))));
+    }
+    *threads = gate_backward_resident<T>(*k, columns ? 2 : 0, false);
+    if (T::kBytes == 4 && residual && slots > 560) *threads = 256;
+    if (T::kBytes == 2 && slots > 1024) *threads = slots <= 2048 ? 64 : (slots <= 4096 ? 128 : 256);
+}
+
 template <class T>
 cudaError_t launch_gate_backward_typed(const GateBackwardArgs &a, int sms, bool pdl, cudaStream_t stream,
                                        uint64_t *launches) {
-    const int64_t most = backward_parts(a.rows, a.n, sms);
+    const int64_t most = gate_parts(a.rows, a.n, sms);
     const bool scalar_gate = a.dgate && a.gate.kind == MRN_FACTOR_SCALAR;
     const bool scalar_scale = a.dscale && a.scale.kind == MRN_FACTOR_SCALAR;
     GateParts parts = {};
@@ -575,13 +590,12 @@ cudaError_t launch_gate_backward_typed(const GateBackwardArgs &a, int sms, bool 
         bool done = false;
         if (mis >= 0) {
             const int64_t slots = a.n / 8;
-            int k = T::kBytes == 2 ? 2 : (slots <= 1024 ? 3 : 4);
-            if (mis != 0 || a.n % 8 != 0) k = T::kBytes == 2 ? 2 : 4;
-            int most_threads = gate_backward_resident<T>(k, parts.res ? 2 : 0);
-            if (slots > 1024) most_threads = slots <= 2048 ? 64 : (slots <= (T::kBytes == 2 ? 4096 : 8192) ? 128 : 256);
-            while (most_threads < gate_backward_resident<T>(k, parts.res ? 2 : 0) && slots > int64_t(kMaxCluster) * k * most_threads) most_threads *= 2;
-            if (most_threads > gate_backward_resident<T>(k, parts.res ? 2 : 0)) most_threads = gate_backward_resident<T>(k, parts.res ? 2 : 0);
-            if (most_threads > 512) most_threads = 512;
+            const bool edge = mis != 0 || a.n % 8 != 0;
+            int k, most_threads;
+            gate_backward_tile<T>(slots, edge, a.dscale != nullptr, parts.res != nullptr, &k, &most_threads);
+            while (most_threads < gate_backward_resident<T>(k, parts.res ? 2 : 0, false) && slots > int64_t(kMaxCluster) * k * most_threads)
+                most_threads *= 2;
+            if (most_threads > gate_backward_resident<T>(k, parts.res ? 2 : 0, false)) most_threads = gate_backward_resident<T>(k, parts.res ? 2 : 0, false);
             const bool few = tile_few_rows(a.rows, a.n, sms);
             if (few) {
                 k = 1;

@@ -37,6 +37,12 @@ __device__ __forceinline__ int sum_six_index(int lane) {
     return (lane >> 4) + ((lane & 8) ? 2 : 0);
 }
 
+// ... and all six for all lanes.
+__device__ __forceinline__ void from_lanes(float (&v)[6], float t) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, t, i < 4 ? (i & 1) * 16 + (i >> 1) * 8 : (i & 1) * 16 + 4);
+}
+
 // Six values over a CTA of at most 16 warps: one barrier; behind it each lane adds four warps' sums
 // of one value, two shuffles join them and six hand them to all lanes.
 struct CtaSumSix {
@@ -72,6 +78,11 @@ template <bool WARP>
 __device__ __forceinline__ bool row_sum_six(float (&v)[6], RowSumSlots<6, false> &s, int &turn, int width,
                                             unsigned cl, unsigned crank, uint32_t stall) {
     if constexpr (WARP) {
+        if (width == 32) {
+            const float t = warp_sum_six(v, static_cast<int>(threadIdx.x & 31));
+            from_lanes(v, t);
+            return true;
+        }
 #pragma unroll
         for (int i = 0; i < 6; ++i) v[i] = group_allsum(v[i], width);
     } else {
@@ -89,9 +100,7 @@ __device__ __forceinline__ bool row_sum_six(float (&v)[6], RowSumSlots<6, false>
 #pragma unroll
             for (int i = 0; i < 6; ++i) x[i] = lane >= cl ? 0.0f : (lane == crank ? v[i] : s.box[p][i][lane]);
             const float t = warp_sum_six(x, static_cast<int>(lane));
-#pragma unroll
-            for (int i = 0; i < 6; ++i)
-                v[i] = __shfl_sync(0xFFFFFFFFu, t, i < 4 ? (i & 1) * 16 + (i >> 1) * 8 : (i & 1) * 16 + 4);
+            from_lanes(v, t);
             if (__syncthreads_or(late)) {
                 if (threadIdx.x == 0) atomicAdd(&g_wait_timeouts, 1u);
                 return false;
@@ -103,9 +112,9 @@ __device__ __forceinline__ bool row_sum_six(float (&v)[6], RowSumSlots<6, false>
 
 // A gate of one value per row travels with its row: one word per lanes that copy together (bf16:
 // the word that holds the element).  A load of it in the loop would hold up every row.
-template <int R, bool EDGE, bool WARP> struct RowGates {
+template <bool EDGE, bool WARP> struct RowGates {
     static constexpr int kTeams = !WARP ? kCtaWarps : (EDGE ? kWarpTileThreads / kEndLanes : kWarpTileThreads);
-    uint32_t w[kTileMaxStages][R][kTeams];
+    uint32_t w[kTileMaxStages][kTeams];
 };
 template <class T> __device__ __forceinline__ uintptr_t row_gate_at(const Factor &gate, int64_t row) {
     return reinterpret_cast<uintptr_t>(gate.p) + static_cast<uintptr_t>(row * T::kBytes);

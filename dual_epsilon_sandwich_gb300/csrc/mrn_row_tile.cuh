@@ -607,7 +607,7 @@ struct TileGrid {
 template <class... Params>
 cudaError_t tile_grid(TileLaunchCache &cache, void (*fn)(Params...), const TileShape &s, int64_t rows, int64_t n,
                       int rows_at_a_time, int elem_bytes, int operands, int most_per_sm, int sms, TileGrid *g,
-                      int64_t beside = 0) {
+                      int64_t beside = 0, int most_stages = kTileMaxStages) {
     *g = TileGrid{};
     int per_sm = 0;
     cudaError_t err = open_tile(cache, fn, s.threads, &per_sm);
@@ -619,7 +619,7 @@ cudaError_t tile_grid(TileLaunchCache &cache, void (*fn)(Params...), const TileS
         g->stages = budget < 0 ? 0 : static_cast<int>(budget / stage);
         if (g->stages >= 2 || per_sm == 1) break;
     }
-    if (g->stages > kTileMaxStages) g->stages = kTileMaxStages;
+    if (g->stages > most_stages) g->stages = most_stages;
     if (g->stages < 1) return cudaSuccess;
     g->shared = stage * g->stages + beside;
     int64_t groups = static_cast<int64_t>(sms) * per_sm;      // CTAs or clusters
