@@ -22,18 +22,23 @@ namespace mrn {
 
 constexpr int kLoopedThreads = 512;
 
+// 1 / sqrt(v) within one unit: rsqrtf and a step of Newton's (0 at infinity, as rsqrtf).  Its error is
+// the whole row's, and does not average out in the sums over rows that scalar factors take.
+__device__ __forceinline__ float inv_sqrt_refined(float v) {
+    const float y = rsqrtf(v);
+    return v < INFINITY ? fmaf(0.5f * y, fmaf(-v * y, y, 1.0f), y) : y;
+}
+
 // What a row's six sums give.
 struct RowScalars {
     float i1, i2;     // inv of the block's row, of the stream's
     float m;          // -i2 * mean(w s) * i2, the factor of xh_s = s i2 in ds
     float q;          // sum_j ds c xh
 };
-template <class InvSqrt>
-__device__ __forceinline__ RowScalars row_scalars(const float (&s)[6], float inv_n, float eps1, float eps2,
-                                                  InvSqrt inv_sqrt_of) {
+__device__ __forceinline__ RowScalars row_scalars(const float (&s)[6], float inv_n, float eps1, float eps2) {
     RowScalars r;
-    r.i1 = inv_sqrt_of(fmaf(s[2], inv_n, eps1));
-    r.i2 = inv_sqrt_of(fmaf(s[0], inv_n, eps2));
+    r.i1 = inv_sqrt_refined(fmaf(s[2], inv_n, eps1));
+    r.i2 = inv_sqrt_refined(fmaf(s[0], inv_n, eps2));
     const float mean = r.i2 * (s[1] * inv_n);
     r.m = -mean * r.i2;
     r.q = r.i1 * fmaf(r.i2, s[3], fmaf(r.m, r.i2 * s[4], s[5]));
@@ -47,28 +52,43 @@ struct GateParts {
     int64_t stride;
 };
 
-// A CTA's share of the scalar factors' gradients, in 64 bits: they sum over all elements, and
-// what they leave behind cancelling is small.
-__device__ __forceinline__ void leave_scalars(double gate, double scale, const GateParts &parts,
-                                              double (&s)[2][kCtaWarps]) {
-    if (!parts.gate && !parts.scale) return;
+// a += v with the rounding's loss kept in b (Knuth's two-sum, "The Art of Computer Programming",
+// volume 2, 4.2.2).
+__device__ __forceinline__ void add_kept(float &a, float &b, float v) {
+    const float s = a + v;
+    const float w = s - a;
+    b += (a - (s - w)) + (v - w);
+    a = s;
+}
+
+// The sum over a warp of values kept that way.
+__device__ __forceinline__ double warp_sum_kept(float a, float b) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-        gate += __shfl_xor_sync(0xFFFFFFFFu, gate, o);
-        scale += __shfl_xor_sync(0xFFFFFFFFu, scale, o);
+        const float c = __shfl_xor_sync(0xFFFFFFFFu, a, o), d = __shfl_xor_sync(0xFFFFFFFFu, b, o);
+        add_kept(a, b, c);
+        b += d;
     }
+    return static_cast<double>(a) + static_cast<double>(b);
+}
+
+// A CTA's share of the scalar factors' gradients, each a sum and what its roundings lost: they are
+// sums over all elements, and what these leave behind cancelling is small.  (In f32 pairs: an SM does
+// two 64-bit additions a clock.)
+__device__ __forceinline__ void leave_scalars(float gate, float gate_lost, float scale, float scale_lost,
+                                              const GateParts &parts, double (&s)[2][kCtaWarps]) {
+    if (!parts.gate && !parts.scale) return;
+    const double g = warp_sum_kept(gate, gate_lost), c = warp_sum_kept(scale, scale_lost);
     if ((threadIdx.x & 31) == 0) {
-        s[0][threadIdx.x >> 5] = gate;
-        s[1][threadIdx.x >> 5] = scale;
+        s[0][threadIdx.x >> 5] = g;
+        s[1][threadIdx.x >> 5] = c;
     }
     __syncthreads();
-    if (threadIdx.x != 0) return;
-    for (int w = 1; w < static_cast<int>(blockDim.x >> 5); ++w) {
-        gate += s[0][w];
-        scale += s[1][w];
-    }
-    if (parts.gate) parts.gate[blockIdx.x] = gate;
-    if (parts.scale) parts.scale[blockIdx.x] = scale;
+    if (threadIdx.x >= 2) return;
+    double sum = 0.0;
+    for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) sum += s[threadIdx.x][w];
+    double *const to = threadIdx.x == 0 ? parts.gate : parts.scale;
+    if (to) to[blockIdx.x] = sum;
 }
 
 // Any width and any alignment: one row per CTA at a time, two passes over it (the second out of
@@ -85,7 +105,7 @@ mrn_gate_backward_looped_kernel(const GateBackwardArgs a, const GateParts parts)
     const float inv_n = 1.0f / static_cast<float>(a.n);
     const int64_t at = static_cast<int64_t>(blockIdx.x) * parts.stride;
     const bool channel = a.gate.kind == MRN_FACTOR_CHANNEL;
-    double gates = 0.0, scales = 0.0;
+    float gates = 0.0f, gates_lost = 0.0f, scales = 0.0f, scales_lost = 0.0f;
     bool fresh = true;
     for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const int64_t e0 = r * a.n;
@@ -102,7 +122,7 @@ mrn_gate_backward_looped_kernel(const GateBackwardArgs a, const GateParts parts)
             if (a.dstream) s[5] = fmaf(ld_elem<T>(a.dstream, e0 + j), cb, s[5]);
         }
         cta_sum(s, slots, turn);
-        const RowScalars k = row_scalars(s, inv_n, a.eps1, a.eps2, [](float v) { return 1.0f / sqrtf(v); });
+        const RowScalars k = row_scalars(s, inv_n, a.eps1, a.eps2);
         const float g = channel ? 1.0f : factor_at<T>(a.gate, r, 0);
         const float c2 = -k.i1 * (g * (k.q * inv_n));
         float gated = 0.0f, scaled = 0.0f;
@@ -129,12 +149,12 @@ mrn_gate_backward_looped_kernel(const GateBackwardArgs a, const GateParts parts)
             gated = fmaf(ds * c, xh, gated);
             scaled = fmaf(ds, res, scaled);
         }
-        gates += gated;
-        scales += scaled;
+        add_kept(gates, gates_lost, gated);
+        add_kept(scales, scales_lost, scaled);
         if (a.dgate && a.gate.kind == MRN_FACTOR_ROW && threadIdx.x == 0) a.dgate[r] = k.q;
         fresh = false;
     }
-    leave_scalars(gates, scales, parts, last);
+    leave_scalars(gates, gates_lost, scales, scales_lost, parts, last);
 }
 
 // Threads that an SM's registers are shared between (the launch bound): what a thread with k
@@ -142,15 +162,6 @@ mrn_gate_backward_looped_kernel(const GateBackwardArgs a, const GateParts parts)
 template <class T> constexpr int gate_backward_resident(int k, int res, bool warp) {
     const int words = k * (8 * (res == 2 ? 4 : 3) + Slot<T>::kWords) + (warp ? 24 : 0);
     return words <= 56 ? 512 : (words <= 64 ? 448 : (words <= 108 ? 384 : 256));
-}
-
-// a += v with the rounding's loss kept in b (Knuth's two-sum, "The Art of Computer Programming",
-// volume 2, 4.2.2).
-__device__ __forceinline__ void add_kept(float &a, float &b, float v) {
-    const float s = a + v;
-    const float w = s - a;
-    b += (a - (s - w)) + (v - w);
-    a = s;
 }
 
 // Rows behind a ring of copies, the column sums in registers over all rows of the CTA (see
@@ -283,7 +294,7 @@ mrn_gate_backward_tile_kernel(const GateBackwardArgs a, const TileArgs t, const 
         }
         const float g = by_row && ok ? row_gate<T>(gates.w[walk.read][tile.team], a.gate, tile.row) : gate;
         if (!row_sum_six<WARP>(s, slots, turn, tile.width, tile.cl, tile.crank, turn == 0 ? t.stall : 0u)) break;
-        const RowScalars q = row_scalars(s, inv_n, a.eps1, a.eps2, [](float v) { return inv_sqrt(v); });
+        const RowScalars q = row_scalars(s, inv_n, a.eps1, a.eps2);
         if (a.dgate && by_row && tile.first == 0 && ok) a.dgate[tile.row] = q.q;
         const float c2 = -q.i1 * (g * (q.q * inv_n)), ig = q.i1 * g;
         const uint64_t i1 = f2_pack(q.i1, q.i1), i2 = f2_pack(q.i2, q.i2), m = f2_pack(q.m, q.m);
@@ -344,7 +355,7 @@ mrn_gate_backward_tile_kernel(const GateBackwardArgs a, const TileArgs t, const 
     }
     cp_async_wait(0);
     row_sum_leave(tile.cl);
-    leave_scalars(static_cast<double>(gate_hi) + gate_lo, static_cast<double>(scale_hi) + scale_lo, parts, last);
+    leave_scalars(gate_hi, gate_lo, scale_hi, scale_lo, parts, last);
     // Column j of a partial row stands at j + 8 - before, so that slots are aligned; the join
     // knows `before` from the row's number.
     constexpr int kSets = RES == 2 ? 3 : 2;
@@ -423,22 +434,25 @@ struct GateJoinArgs {
 template <class T, int WARPS, int C, int kJoinFlight>
 __global__ void __launch_bounds__(WARPS * 32) mrn_gate_join_kernel(const GateJoinArgs a) {
     __shared__ float sums[WARPS][C * 32];
-    __shared__ double scalar[WARPS];
+    __shared__ double scalar[4];
     pdl_enter();
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;
     if (static_cast<int>(blockIdx.x) == a.columns) {
         const double *from = blockIdx.y == 0 ? a.from.gate : (blockIdx.y == 1 ? a.from.scale : nullptr);
         if (!from) return;
-        double v = 0.0;
-        for (int64_t i = threadIdx.x; i < a.scalars; i += WARPS * 32) v += from[i];
+        // (four warps: see leave_scalars on 64-bit additions)
+        if (warp < 4) {
+            double v = 0.0;
+            for (int64_t i = threadIdx.x; i < a.scalars; i += 128) v += from[i];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-        if (lane == 0) scalar[warp] = v;
+            for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+            if (lane == 0) scalar[warp] = v;
+        }
         __syncthreads();
-        if (threadIdx.x != 0) return;
-        for (int w = 1; w < WARPS; ++w) v += scalar[w];
-        *(blockIdx.y == 0 ? a.dgate : a.dscale) = static_cast<float>(v);
+        if (threadIdx.x == 0)
+            *(blockIdx.y == 0 ? a.dgate : a.dscale) =
+                static_cast<float>((scalar[0] + scalar[1]) + (scalar[2] + scalar[3]));
         return;
     }
     const float *part = blockIdx.y == 0 ? a.from.pre : (blockIdx.y == 1 ? a.from.post : a.from.res);
@@ -518,53 +532,83 @@ struct GateBackwardLaunch {
     cudaError_t err;    // out
 };
 
+// Whether gate_backward_tile chooses this form for any call (rows that share a warp, few rows: all).
+template <class T> constexpr bool gate_backward_chosen(int k, bool edge, bool warp, int res) {
+    if (warp || k == 1 || k == 4) return true;
+    if (k == 3) return res == 0 || (T::kBytes == 2 && res == 1);
+    return T::kBytes == 4 || !edge || res == 2;
+}
+
 // Whether the call was launched; false: it takes the looped kernel.
 template <class T, int K, bool EDGE, bool WARP, int RES>
 bool launch_gate_backward_tile(const GateBackwardArgs &a, const GateParts &parts, const TileShape &p,
                                GateBackwardLaunch &l) {
-    static TileLaunchCache cache;
-    const auto fn = mrn_gate_backward_tile_kernel<T, K, EDGE, WARP, RES>;
-    const int operands = 3 + (a.dstream ? 1 : 0) + (RES ? 1 : 0);
-    const int64_t alpha = a.scale.kind == MRN_FACTOR_CHANNEL ? int64_t(K) * p.threads * 8 * T::kBytes : 0;
-    TileGrid g;
-    // (WARP: the epilogue's rows have room for the ends)
-    l.err = tile_grid(cache, fn, p, a.rows, a.n, 1, T::kBytes, operands, gate_parts_per_sm(a.n), l.sms, &g, alpha + (WARP ? 1024 : 0));
-    if (l.err != cudaSuccess) return true;
-    l.parts = g.ctas / p.cluster;
-    l.ctas = g.ctas;
-    if (g.stages < 1 || l.parts > l.most_parts) return false;   // (the workspace holds no more)
-    const TileArgs t = {p.lanes, g.stages, p.mis, a.stall};
-    l.err = launch_tile(fn, p, g.ctas, g.shared, l.pdl, l.stream, l.launches, a, t, parts,
-                        static_cast<uint32_t>(g.shared - alpha));
-    return true;
+    if constexpr (!gate_backward_chosen<T>(K, EDGE, WARP, RES)) {
+        return false;
+    } else {
+        static TileLaunchCache cache;
+        const auto fn = mrn_gate_backward_tile_kernel<T, K, EDGE, WARP, RES>;
+        const int operands = 3 + (a.dstream ? 1 : 0) + (RES ? 1 : 0);
+        const int64_t alpha = a.scale.kind == MRN_FACTOR_CHANNEL ? int64_t(K) * p.threads * 8 * T::kBytes : 0;
+        TileGrid g;
+        // (WARP: the epilogue's rows have room for the ends)
+        l.err = tile_grid(cache, fn, p, a.rows, a.n, 1, T::kBytes, operands, gate_parts_per_sm(a.n), l.sms, &g,
+                          alpha + (WARP ? 1024 : 0));
+        if (l.err != cudaSuccess) return true;
+        l.parts = g.ctas / p.cluster;
+        l.ctas = g.ctas;
+        if (g.stages < 1 || l.parts > l.most_parts) return false;   // (the workspace holds no more)
+        const TileArgs t = {p.lanes, g.stages, p.mis, a.stall};
+        l.err = launch_tile(fn, p, g.ctas, g.shared, l.pdl, l.stream, l.launches, a, t, parts,
+                            static_cast<uint32_t>(g.shared - alpha));
+        return true;
+    }
+}
+
+template <class T, int K, bool EDGE, bool WARP>
+bool launch_gate_backward_res(const GateBackwardArgs &a, const GateParts &parts, const TileShape &p,
+                              GateBackwardLaunch &l) {
+    if (!a.dscale) return launch_gate_backward_tile<T, K, EDGE, WARP, 0>(a, parts, p, l);
+    return parts.res ? launch_gate_backward_tile<T, K, EDGE, WARP, 2>(a, parts, p, l)
+                     : launch_gate_backward_tile<T, K, EDGE, WARP, 1>(a, parts, p, l);
 }
 
 template <class T, int K, bool WARP>
 bool launch_gate_backward_k(const GateBackwardArgs &a, const GateParts &parts, const TileShape &p,
                             GateBackwardLaunch &l) {
-    const int res = !a.dscale ? 0 : (parts.res ? 2 : 1);
-    if (p.edge)
-        return res == 0   ? launch_gate_backward_tile<T, K, true, WARP, 0>(a, parts, p, l)
-               : res == 1 ? launch_gate_backward_tile<T, K, true, WARP, 1>(a, parts, p, l)
-                          : launch_gate_backward_tile<T, K, true, WARP, 2>(a, parts, p, l);
-    return res == 0   ? launch_gate_backward_tile<T, K, false, WARP, 0>(a, parts, p, l)
-           : res == 1 ? launch_gate_backward_tile<T, K, false, WARP, 1>(a, parts, p, l)
-                      : launch_gate_backward_tile<T, K, false, WARP, 2>(a, parts, p, l);
+    return p.edge ? launch_gate_backward_res<T, K, true, WARP>(a, parts, p, l)
+                  : launch_gate_backward_res<T, K, false, WARP>(a, parts, p, l);
 }
 
-// Slots per thread (k) for rows of a CTA, and threads of one at most.
+// Slots per thread (k) for rows of a CTA, and threads of one at most.  Measured on GB300 (us), a stream's
+// gradient with it, 805 MB a call (654 at 6656 and 6655; 940 and 763 with the residual's scale):
+//   bf16  k 1, 2, 3, 4:  n = 1032 202, 187, 165, 209;  1280 (1 GB) 208, 189, 179, 211;  2048 168, 146, 143,
+//         143;  2560 198, 147, 141, 174;  4096 178, 139, 142, 144;  4095 198, 151, 145, 148;  5120 261,
+//         164, 165, 173;  6656 246, 163, 160, 155;  8192 222, 152, 149, 142
+//         a scale per channel: 2048 175, 164, 195, 174;  4096 191, 177, 188, 169;  4095 206, 195, 232,
+//         172;  8192 244, 219, 191, 159;  a scalar one: 4096 193, 170, 166, 169
+//   f32   n = 1032 146, 179, 166, 225;  1280 (1 GB) 187, 172, 169, 220;  2048 140, 147, 135, 135;  4096 142,
+//         134, 130, 139;  4095 162, 194, 148, 156;  5120 147, 144, 139, 134;  6656 143, 117, 139, 141;  6655
+//         165, 154, 155, 156;  8192 166, 168, 162, 159;  12288 183, 152, 156, 140;  16384 175, 170, 188, 174
+//         a scale per channel: 2048 167, 168, 195, 163;  4096 160, 157, 160, 165;  6656, two CTAs a row,
+//         151 with one slot, 157, 163, 167
+// At 6656 f32 a row's four operands take 106 KB: two stages fit, and with two slots 13 warps.
 template <class T> void gate_backward_tile(int64_t slots, bool edge, bool residual, bool columns, int *k, int *threads) {
     if (T::kBytes == 2) {
         if (columns) *k = slots <= 384 ? 2 : 4;
         else *k = slots > 640 ? 4 : (slots <= 400 || edge ? 3 : 2);
     } else if (residual) {
-        *k = slots <= 560 ? 2 : 1;
+        *k = slots <= 560 ? 2 : (slots <= 4096 ? 1 : 4);
     } else {
-        *k = slots <= 160 ? 1 : (slots <= 384 ? 4 : (slots <= 560 ? 3 : (slots <= 700 ? 4 : (slots <= 896 ? 2 : 4))));
+        *k = slots <= 144 ? 1 : (slots <= 560 && slots > 384 ? 3 : (slots > 700 && slots <= 896 ? 2 : 4));
+        if (slots > 144 && slots <= 192) *k = 3;
     }
-    *threads = gate_backward_resident<T>(*k, columns ? 2 : 0, false);
+    const int most = gate_backward_resident<T>(*k, columns ? 2 : 0, false);
+    *threads = most;
     if (T::kBytes == 4 && residual && slots > 560) *threads = 256;
     if (T::kBytes == 2 && slots > 1024) *threads = slots <= 2048 ? 64 : (slots <= 4096 ? 128 : 256);
+    while (*threads < most && slots > int64_t(kMaxCluster) * *k * *threads) *threads *= 2;
+    if (*threads > most) *threads = most;
 }
 
 template <class T>
@@ -593,9 +637,6 @@ cudaError_t launch_gate_backward_typed(const GateBackwardArgs &a, int sms, bool 
             const bool edge = mis != 0 || a.n % 8 != 0;
             int k, most_threads;
             gate_backward_tile<T>(slots, edge, a.dscale != nullptr, parts.res != nullptr, &k, &most_threads);
-            while (most_threads < gate_backward_resident<T>(k, parts.res ? 2 : 0, false) && slots > int64_t(kMaxCluster) * k * most_threads)
-                most_threads *= 2;
-            if (most_threads > gate_backward_resident<T>(k, parts.res ? 2 : 0, false)) most_threads = gate_backward_resident<T>(k, parts.res ? 2 : 0, false);
             const bool few = tile_few_rows(a.rows, a.n, sms);
             if (few) {
                 k = 1;

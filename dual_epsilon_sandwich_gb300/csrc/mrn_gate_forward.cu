@@ -56,7 +56,7 @@ template <class T> constexpr int gate_threads(int k, bool ach) {
 
 // Stages of the tiles' ring at most: with more copies in flight than two stages of each CTA, reads and
 // writes get in each other's way in DRAM (4096 x 6655 f32 78.9 us with four, 76.5 with two; 16384 x
-// 4095 bf16 93.1, 89.0; 32768 x 4096 f32 351, 332).
+// 4095 bf16 93.1, 89.0; 32768 x 4096 f32 351, 332; but one slot of bf16, 16384 x 4096, 87.6 and 89.0).
 constexpr int kGateStages = 2;
 // Threads of the row kernel at most (two CTAs of that size share an SM's registers).
 constexpr int kGateRowThreads = 32 * kCtaWarps;
@@ -180,7 +180,8 @@ bool launch_gate_tile(const GateArgs &a, const TileShape &p, int sms, bool pdl, 
     static TileLaunchCache cache;
     const auto fn = mrn_gate_tile_kernel<T, K, EDGE, WARP, ACH>;
     TileGrid g;
-    *err = tile_grid(cache, fn, p, a.rows, a.n, 1, T::kBytes, 2, 32, sms, &g, 0, kGateStages);
+    *err = tile_grid(cache, fn, p, a.rows, a.n, 1, T::kBytes, 2, 32, sms, &g, 0,
+                     T::kBytes == 2 && K == 1 && !EDGE && !WARP ? kTileMaxStages : kGateStages);
     if (*err != cudaSuccess) return true;
     if (g.stages < 1) return false;
     const TileArgs t = {p.lanes, g.stages, p.mis, a.stall};
@@ -292,6 +293,7 @@ template <class T> int gate_row_slots(const GateArgs &a, int mis, int sms) {
     if (mis != 0 || a.n % 8 != 0 || weights % 16 != 0 || a.rows > 0x7FFFFFFF) return 0;
     const int64_t slots = a.n / 8;
     if (a.rows <= 2LL * sms && slots > 16 && slots <= kGateRowThreads) return 1;
+    if (a.rows <= sms) return 0;
     if (T::kBytes == 2) return slots >= 128 && slots <= 256 && slots % 64 == 0 ? 2 : 0;
     return slots < 64 || slots > 2 * kGateRowThreads ? 0 : (slots <= 128 ? 1 : 2);
 }

@@ -136,7 +136,8 @@ def test_backward(i, dtype):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("rows,n", [(3, 16), (100, 5), (700, 130), (300, 1000), (4, 6656),
                                     (310, 4096), (320, 4095), (155, 16391), (5, 33000),
-                                    (2, 270001)])
+                                    (2, 270001), (400, 1024), (350, 2048), (330, 8192), (900, 512),
+                                    (320, 1536)])
 def test_every_pair_of_factors(rows, n, dtype):
     b, res, g1, g2 = operands(1, rows, n, dtype)
     s, dn, ds = (make(10 + k, rows, n, dtype) for k in range(3))
