@@ -10,7 +10,9 @@ namespace mrn {
 constexpr int kLoopedThreads = 512;
 
 // Any width and any alignment: one row per CTA at a time, three passes over it (the second and
-// third out of L2), element by element.
+// third out of L2), element by element.  For operands that do not share an offset and rows wider
+// than a cluster holds.  Bound by its accesses of one element: 16384 x 4096 bf16 414 us (the tiles:
+// 89).
 template <class T>
 __global__ void __launch_bounds__(kLoopedThreads) mrn_gate_looped_kernel(const GateArgs a) {
     __shared__ CtaSum slots;
@@ -45,7 +47,8 @@ __global__ void __launch_bounds__(kLoopedThreads) mrn_gate_looped_kernel(const G
 
 // Threads that an SM's registers are shared between (the launch bound), from what a thread
 // holds: k slots of the row, of gamma_post with the gate in f32, of gamma_pre and, ACH, of a
-// scale per channel.
+// scale per channel.  (It does not count what rows that share a warp take beside them: eight of
+// those bf16 forms spill, 36 to 160 bytes.)
 template <class T> constexpr int gate_resident(int k, bool ach) {
     const int words = k * ((2 + ach) * Slot<T>::kWords + 8);
     return words <= 16 ? 1024 : (words <= 32 ? 768 : (words <= 44 ? 640 : (words <= 72 ? 512 : (words <= 104 ? 384 : 256))));
@@ -74,7 +77,13 @@ __device__ __forceinline__ void ld_weights(Slot<F32> &s, const void *p) {
 
 // Rows held in registers between their copy and their outputs (see mrn_row_tile.cuh): every
 // operand is read once, every output written once, and a row has two sums, the second over the
-// rounded stream.  ACH: the residual has a scale per channel.
+// rounded stream.  ACH: the residual has a scale per channel.  Measured on GB300: 16384 x 4096 bf16
+// 88 to 90 us (6.0 TB/s, 88 % of the copy's rate), 4096 x 6655 f32 73 to 75 us (5.9 TB/s), 1 x 6656 f32
+// 2.7 us, a launch and two sums over a cluster.
+//   What bounds it: bf16 the instructions (issued in 68 % of cycles, the conversions most of them),
+// f32 at odd pitches 13 warps that wait for shared memory and the barrier, and everywhere what reads
+// ahead and writes of a persistent grid cost in DRAM: aligned f32 rows take 10 % less in the kernel
+// below, whose CTAs come and go.
 template <class T, int K, bool EDGE, bool WARP, bool ACH>
 __global__ void __launch_bounds__(gate_resident<T>(K, ACH))
 mrn_gate_tile_kernel(const GateArgs a, const TileArgs t) {
@@ -199,8 +208,14 @@ bool launch_gate_k(const GateArgs &a, const TileShape &p, int sms, bool pdl, cud
                   : launch_gate_tile<T, K, false, WARP, false>(a, p, sms, pdl, stream, launches, err);
 }
 
-// One row per CTA, K slots of eight elements to a thread, none of them kept from row to row: aligned
-// rows only.  The grid holds all rows, and an SM as many of them as its registers do.
+// One row per CTA, K slots of eight elements to a thread, nothing kept from row to row: aligned
+// rows only.  The grid holds all rows, and an SM as many of them as its registers do; the weights come
+// out of L1 for each row, behind the barriers, where the row's own registers are free for them.
+// Measured on GB300: 8192 x 4096 f32 80.8 us (6.65 TB/s, 98 % of the copy's rate), 4096 x 6656 f32 70 to
+// 71 (a gate per channel; 66.7 without one, 96 %), 32768 x 2048 bf16 85.6 (6.3 TB/s).
+//   What bounds it: memory; at 6656, where two CTAs fill an SM's registers, the waits for the weights
+// behind the barriers (long scoreboard 12 cycles per issue).  Rows of fewer bytes than 8 KB would be
+// bound by the start of their CTAs, about one a nanosecond: they take the tiles.
 template <class T, int K>
 __global__ void __launch_bounds__(kGateRowThreads, 2)
 mrn_gate_row_kernel(const GateArgs a) {
@@ -307,11 +322,11 @@ cudaError_t launch_gate_row(const GateArgs &a, bool pdl, cudaStream_t stream, ui
 // Slots per thread (k) for rows of a CTA, and threads of one at most.  Measured on GB300 (us, k 1, 2,
 // 4; 537 MB a call, 436 at 6655):
 //   bf16  n = 2560 93.0, 92.9, 91.9;  4095 108, 90.3, 90.3;  4096 87.6, 92.1, 90.3;  5120 113, 93.7,
-//         91.0;  6656 116, 95.8, 92.4;  8192 125, 87.5, 91.7
+//         91.0;  6656 116, 95.8, 92.4;  8192 125, 87.5, 91.7;  4096 with a scale per channel 103, 93.1, 92.0
 //   f32   n = 1032 99.2, 99.2, 96.1;  4095 89.6, 97.0, 97.8;  6655 113, 76.5, 76.4;  12288 122, 97.2, 92.4
 template <class T> void gate_tile(int64_t slots, bool edge, bool ach, int *k, int *threads) {
     if (T::kBytes == 2) {
-        *k = slots > 448 && slots <= 512 && !edge ? 1 : (slots >= 960 && slots <= 1024 ? 2 : 4);
+        *k = slots > 448 && slots <= 512 && !edge && !ach ? 1 : (slots >= 960 && slots <= 1024 ? 2 : 4);
         *threads = slots > 2048 ? 128 : 512;
     } else {
         *k = slots <= 512 ? 1 : (slots <= 1024 || slots > 1536 ? 2 : 4);
