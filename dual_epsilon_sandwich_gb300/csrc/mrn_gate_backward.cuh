@@ -69,7 +69,8 @@ __device__ __forceinline__ double warp_sum_kept(float a, float b) {
         add_kept(a, b, c);
         b += d;
     }
-    return static_cast<double>(a) + static_cast<double>(b);
+    // (an infinite sum has lost NaN)
+    return fabsf(a) < INFINITY ? static_cast<double>(a) + static_cast<double>(b) : static_cast<double>(a);
 }
 
 // A CTA's share of the scalar factors' gradients, each a sum and what its roundings lost: they are
@@ -608,7 +609,7 @@ template <class T> void gate_backward_tile(int64_t slots, bool edge, bool residu
         if (columns) *k = slots <= 384 ? 2 : 4;
         else *k = slots > 640 ? 4 : (slots <= 400 || edge ? 3 : 2);
     } else if (residual) {
-        *k = slots <= 560 ? 2 : (slots <= 4096 ? 1 : 4);
+        *k = slots <= 160 || slots > 560 ? (slots <= 4096 ? 1 : 4) : 2;
     } else {
         *k = slots <= 144 ? 1 : (slots <= 560 && slots > 384 ? 3 : (slots > 700 && slots <= 896 ? 2 : 4));
         if (slots > 144 && slots <= 192) *k = 3;
@@ -652,7 +653,10 @@ cudaError_t launch_gate_backward_typed(const GateBackwardArgs &a, int sms, bool 
                 k = 1;
                 most_threads = tile_few_threads(a.rows, a.n, sms);
             }
-            const TileShape p = tile_shape(a.n, mis, k, most_threads, few);
+            // (f32 rows of more slots than three for each lane of a warp: four spill; 32768 x 1024 167 us in
+            // warps, 142 in CTAs of 128 threads)
+            const bool apart = T::kBytes == 4 && slots > 96 && !edge;
+            const TileShape p = tile_shape(a.n, mis, k, most_threads, few || apart);
             if (p.ok && p.warp) {
                 done = p.k == 1   ? launch_gate_backward_k<T, 1, true>(a, parts, p, l)
                        : p.k == 2 ? launch_gate_backward_k<T, 2, true>(a, parts, p, l)

@@ -2,6 +2,7 @@
 import os
 import subprocess
 import sys
+import threading
 import time
 
 import numpy as np
@@ -216,6 +217,22 @@ def test_infinities_stay_in_their_rows(n, dtype):
     assert np.isnan(outs[1][2][[2, 4, 5]]).any(1).all()
 
 
+@pytest.mark.parametrize("rows,n", [(9, 40), (700, 512), (5, 4096), (320, 4095), (7, 140001)])
+def test_an_infinite_scalar_gradient_is_infinite(rows, n):
+    """One infinite incoming gradient makes the sums over all elements infinite, of its sign, where
+    the formula's other terms are finite."""
+    b, _, g1, g2 = (t.cuda() for t in operands(33, rows, n, "f32"))
+    s, res, ds = make(34, rows, n, "f32").cuda(), make(35, rows, n, "f32").cuda(), torch.zeros(rows, n, device="cuda")
+    one = torch.ones(1, device="cuda")
+    for sign in (1.0, -1.0):
+        ds[rows // 2, n // 3] = sign * float("inf")
+        got = mrn.norm_gate_residual_norm_backward(torch.zeros_like(b), b, s, g1, g2, one, one,
+                                                   residual=res, dstream=ds)
+        at = rows // 2, n // 3
+        assert float(got[5]) == sign * float("inf") * float(res[at].sign())
+        assert float(got[4]) == sign * float("inf") * float((b[at] * g1[at[1]]).sign())
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("rows,n", [(5, 33), (40, 1023), (700, 512), (3, 20001), (1501, 1023),
                                     (2000, 99), (7, 140001)])
@@ -328,6 +345,40 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(p, q) for p, q in zip(got[i], want[i]))
+
+
+def test_several_host_threads():
+    """Calls of several threads, each on a stream of its own, give the bits of calls in turn."""
+    rows, n = 400, 1000
+    sets = []
+    for i in range(4):
+        b, res, g1, g2 = (t.cuda() for t in operands(110 + 10 * i, rows, n, "f32"))
+        sets.append((b, res, g1, g2, *(t.cuda() for t in factors(i, rows, n, "f32", "scalar", "channel"))))
+
+    def step(v):
+        s, y = mrn.norm_gate_residual_norm(*v)
+        grads = mrn.norm_gate_residual_norm_backward(y, v[0], s, v[2], v[3], v[4], v[5], residual=v[1])
+        norm, grads = mrn.clip_grad_norm(grads, 0.5)
+        return (s, y, norm, *grads)
+
+    want = [step(v) for v in sets]
+    torch.cuda.synchronize()
+    got = [None] * len(sets)
+
+    def run(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(10):
+                got[i] = step(sets[i])
+        stream.synchronize()
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(sets))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for a, c in zip(got, want):
+        assert all(torch.equal(p, q) for p, q in zip(a, c))
 
 
 def test_captured_tail_takes_the_factors_of_its_replay():
