@@ -272,7 +272,9 @@ typedef enum mrn_factor {
  * infinity or NaN of the block.  The two factors of a channel (gate and gamma_post) are
  * multiplied first, in f32; bf16: out_stream is rounded once and normed is computed from
  * the rounded values, as in mrn_norm_residual_norm.
- * Speed, alignment and geometry: as of the training operations below.
+ * Speed, alignment and geometry: as of the training operations below (bf16 with a scale per
+ * channel: rows of up to 196,608 elements at full speed); weights and factors of rows that
+ * are all aligned should be 16-byte aligned too.
  */
 mrn_status mrn_norm_gate_residual_norm(const void *block_out, const void *residual,
                                        const void *gamma_post, const void *gamma_pre,
