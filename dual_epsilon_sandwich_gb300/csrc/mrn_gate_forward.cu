@@ -47,14 +47,15 @@ __global__ void __launch_bounds__(kLoopedThreads) mrn_gate_looped_kernel(const G
 
 // Threads that an SM's registers are shared between (the launch bound), from what a thread
 // holds: k slots of the row, of gamma_post with the gate in f32, of gamma_pre and, ACH, of a
-// scale per channel.  (It does not count what rows that share a warp take beside them: eight of
-// those bf16 forms spill, 36 to 160 bytes.)
-template <class T> constexpr int gate_resident(int k, bool ach) {
-    const int words = k * ((2 + ach) * Slot<T>::kWords + 8);
+// scale per channel, and what rows that share a warp take beside them (distances of their own: without
+// it eight bf16 forms spilled, and 65536 x 1023 took 124 us against 100, 65536 x 511 56 against 45; two
+// still do, four slots with a scale per channel).
+template <class T> constexpr int gate_resident(int k, bool ach, bool warp) {
+    const int words = k * ((2 + ach) * Slot<T>::kWords + 8) + (warp ? 20 : 0);
     return words <= 16 ? 1024 : (words <= 32 ? 768 : (words <= 44 ? 640 : (words <= 72 ? 512 : (words <= 104 ? 384 : 256))));
 }
 template <class T> constexpr int gate_threads(int k, bool ach) {
-    return gate_resident<T>(k, ach) < 512 ? gate_resident<T>(k, ach) : 512;
+    return gate_resident<T>(k, ach, false) < 512 ? gate_resident<T>(k, ach, false) : 512;
 }
 
 // Stages of the tiles' ring at most: with more copies in flight than two stages of each CTA, reads and
@@ -85,7 +86,7 @@ __device__ __forceinline__ void ld_weights(Slot<F32> &s, const void *p) {
 // ahead and writes of a persistent grid cost in DRAM: aligned f32 rows take 10 % less in the kernel
 // below, whose CTAs come and go.
 template <class T, int K, bool EDGE, bool WARP, bool ACH>
-__global__ void __launch_bounds__(gate_resident<T>(K, ACH))
+__global__ void __launch_bounds__(gate_resident<T>(K, ACH, WARP))
 mrn_gate_tile_kernel(const GateArgs a, const TileArgs t) {
     extern __shared__ __align__(16) unsigned char ring_bytes[];
     __shared__ RowSumSlots<1, T::kBytes == 2> slots;
