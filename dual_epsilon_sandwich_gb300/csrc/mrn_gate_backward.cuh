@@ -543,11 +543,47 @@ struct GateBackwardLaunch {
     cudaError_t err;    // out
 };
 
-// Whether gate_backward_tile chooses this form for any call (rows that share a warp, few rows: all).
+// Slots per thread (k) for rows of a CTA.  Measured on GB300 (us), a stream's
+// gradient with it, 805 MB a call (654 at 6656 and 6655; 940 and 763 with the residual's scale):
+//   bf16  k 1, 2, 3, 4:  n = 1032 202, 187, 165, 209;  1280 (1 GB) 208, 189, 179, 211;  2048 168, 146, 143,
+//         143;  2560 198, 147, 141, 174;  4096 178, 139, 142, 144;  4095 198, 151, 145, 148;  5120 261,
+//         164, 165, 173;  6656 246, 163, 160, 155;  8192 222, 152, 149, 142
+//         a scale per channel: 2048 175, 164, 195, 174;  4096 191, 177, 188, 169;  4095 206, 195, 232,
+//         172;  8192 244, 219, 191, 159;  a scalar one: 4096 193, 170, 166, 169
+//   f32   n = 1032 146, 179, 166, 225;  1280 (1 GB) 187, 172, 169, 220;  2048 140, 147, 135, 135;  4096 142,
+//         134, 130, 139;  4095 162, 194, 148, 156;  5120 147, 144, 139, 134;  6656 143, 117, 139, 141;  6655
+//         165, 154, 155, 156;  8192 166, 168, 162, 159;  12288 183, 152, 156, 140;  16384 175, 170, 188, 174
+//         a scale per channel: 2048 167, 168, 195, 163;  4096 160, 157, 160, 165;  6656, two CTAs a row,
+//         151 with one slot, 157, 163, 167
+// At 6656 f32 a row's four operands take 106 KB: two stages fit, and with two slots 13 warps.
+template <class T> constexpr int gate_backward_slots(int64_t slots, bool edge, bool residual, bool columns) {
+    if (T::kBytes == 2) {
+        if (columns) return slots <= 384 ? 2 : 4;
+        return slots > 640 ? 4 : (slots <= 400 || edge ? 3 : 2);
+    }
+    if (residual) return slots <= 160 || slots > 560 ? (slots <= 4096 ? 1 : 4) : 2;
+    if (slots <= 144) return 1;
+    if (slots <= 192) return 3;
+    return slots <= 560 && slots > 384 ? 3 : (slots > 700 && slots <= 896 ? 2 : 4);
+}
+
+// Threads of a CTA at most, for that many slots per thread.
+template <class T> int gate_backward_threads(int64_t slots, int k, bool residual, bool columns) {
+    const int most = gate_backward_resident<T>(k, columns ? 2 : 0, false);
+    int threads = most;
+    if (T::kBytes == 4 && residual && slots > 560) threads = 256;
+    if (T::kBytes == 2 && slots > 1024) threads = slots <= 2048 ? 64 : (slots <= 4096 ? 128 : 256);
+    while (threads < most && slots > int64_t(kMaxCluster) * k * threads) threads *= 2;
+    return threads > most ? most : threads;
+}
+
+// Whether any call takes this form: the forms that are compiled.  Rows that share a warp take all
+// of them, few rows one slot, and other rows of a CTA what the rule above gives for some width.
 template <class T> constexpr bool gate_backward_chosen(int k, bool edge, bool warp, int res) {
-    if (warp || k == 1 || k == 4) return true;
-    if (k == 3) return res == 0 || (T::kBytes == 2 && res == 1);
-    return T::kBytes == 4 || !edge || res == 2;
+    if (warp || k == 1) return true;
+    for (int slots = 1; slots <= kMaxCluster * kTileMaxThreads * 4; ++slots)
+        if (gate_backward_slots<T>(slots, edge, res != 0, res == 2) == k) return true;
+    return false;
 }
 
 // Whether the call was launched; false: it takes the looped kernel.
@@ -555,7 +591,8 @@ template <class T, int K, bool EDGE, bool WARP, int RES>
 bool launch_gate_backward_tile(const GateBackwardArgs &a, const GateParts &parts, const TileShape &p,
                                GateBackwardLaunch &l) {
     if constexpr (!gate_backward_chosen<T>(K, EDGE, WARP, RES)) {
-        return false;
+        l.err = cudaErrorInvalidDeviceFunction;     // (no call comes here)
+        return true;
     } else {
         static TileLaunchCache cache;
         const auto fn = mrn_gate_backward_tile_kernel<T, K, EDGE, WARP, RES>;
@@ -591,37 +628,6 @@ bool launch_gate_backward_k(const GateBackwardArgs &a, const GateParts &parts, c
                   : launch_gate_backward_res<T, K, false, WARP>(a, parts, p, l);
 }
 
-// Slots per thread (k) for rows of a CTA, and threads of one at most.  Measured on GB300 (us), a stream's
-// gradient with it, 805 MB a call (654 at 6656 and 6655; 940 and 763 with the residual's scale):
-//   bf16  k 1, 2, 3, 4:  n = 1032 202, 187, 165, 209;  1280 (1 GB) 208, 189, 179, 211;  2048 168, 146, 143,
-//         143;  2560 198, 147, 141, 174;  4096 178, 139, 142, 144;  4095 198, 151, 145, 148;  5120 261,
-//         164, 165, 173;  6656 246, 163, 160, 155;  8192 222, 152, 149, 142
-//         a scale per channel: 2048 175, 164, 195, 174;  4096 191, 177, 188, 169;  4095 206, 195, 232,
-//         172;  8192 244, 219, 191, 159;  a scalar one: 4096 193, 170, 166, 169
-//   f32   n = 1032 146, 179, 166, 225;  1280 (1 GB) 187, 172, 169, 220;  2048 140, 147, 135, 135;  4096 142,
-//         134, 130, 139;  4095 162, 194, 148, 156;  5120 147, 144, 139, 134;  6656 143, 117, 139, 141;  6655
-//         165, 154, 155, 156;  8192 166, 168, 162, 159;  12288 183, 152, 156, 140;  16384 175, 170, 188, 174
-//         a scale per channel: 2048 167, 168, 195, 163;  4096 160, 157, 160, 165;  6656, two CTAs a row,
-//         151 with one slot, 157, 163, 167
-// At 6656 f32 a row's four operands take 106 KB: two stages fit, and with two slots 13 warps.
-template <class T> void gate_backward_tile(int64_t slots, bool edge, bool residual, bool columns, int *k, int *threads) {
-    if (T::kBytes == 2) {
-        if (columns) *k = slots <= 384 ? 2 : 4;
-        else *k = slots > 640 ? 4 : (slots <= 400 || edge ? 3 : 2);
-    } else if (residual) {
-        *k = slots <= 160 || slots > 560 ? (slots <= 4096 ? 1 : 4) : 2;
-    } else {
-        *k = slots <= 144 ? 1 : (slots <= 560 && slots > 384 ? 3 : (slots > 700 && slots <= 896 ? 2 : 4));
-        if (slots > 144 && slots <= 192) *k = 3;
-    }
-    const int most = gate_backward_resident<T>(*k, columns ? 2 : 0, false);
-    *threads = most;
-    if (T::kBytes == 4 && residual && slots > 560) *threads = 256;
-    if (T::kBytes == 2 && slots > 1024) *threads = slots <= 2048 ? 64 : (slots <= 4096 ? 128 : 256);
-    while (*threads < most && slots > int64_t(kMaxCluster) * *k * *threads) *threads *= 2;
-    if (*threads > most) *threads = most;
-}
-
 template <class T>
 cudaError_t launch_gate_backward_typed(const GateBackwardArgs &a, int sms, bool pdl, cudaStream_t stream,
                                        uint64_t *launches) {
@@ -646,13 +652,11 @@ cudaError_t launch_gate_backward_typed(const GateBackwardArgs &a, int sms, bool 
         if (mis >= 0) {
             const int64_t slots = a.n / 8;
             const bool edge = mis != 0 || a.n % 8 != 0;
-            int k, most_threads;
-            gate_backward_tile<T>(slots, edge, a.dscale != nullptr, parts.res != nullptr, &k, &most_threads);
+            const bool residual = a.dscale != nullptr, columns = parts.res != nullptr;
             const bool few = tile_few_rows(a.rows, a.n, sms);
-            if (few) {
-                k = 1;
-                most_threads = tile_few_threads(a.rows, a.n, sms);
-            }
+            const int k = few ? 1 : gate_backward_slots<T>(slots, edge, residual, columns);
+            const int most_threads = few ? tile_few_threads(a.rows, a.n, sms)
+                                         : gate_backward_threads<T>(slots, k, residual, columns);
             // (f32 rows of more slots than three for each lane of a warp: four spill; 32768 x 1024 167 us in
             // warps, 142 in CTAs of 128 threads)
             const bool apart = T::kBytes == 4 && slots > 96 && !edge;
