@@ -11,6 +11,9 @@
 //   S1 = sum s^2, S2 = sum w s, S3 = sum b^2, S4 = sum w c b, S5 = sum s c b, S6 = sum dstream c b
 // q = i1 * (i2 * (S4 - (i2 S2 / n) * (i2 S5)) + S6): the sum of ds c xh term by term, so that what
 // cancels in it is what cancels in ds itself.
+// The products are of the operands as they are, since i1 and i2 are not known yet: rows whose
+// |dn| |b| add up past f32's largest number are outside of the operation's range, as the public
+// header says.  (Products of xh would take a second reduction.)
 //   The column sums are taken on the same pass: every CTA adds up the rows it handles (fixed
 // rows, in order) and leaves a row of partial sums per set in the workspace, which a second
 // launch adds in order.  No atomics: the result does not depend on which CTA ran when.

@@ -914,7 +914,9 @@ def norm_gate_residual_norm_backward(dnormed, block_out, out_stream, gamma_post,
     of norm_residual_norm.  The last four are float32; dgate is None without a gate, dres_scale
     without a res_scale or without residual (the forward's, not updated in place).  dstream, when
     given, is the gradient that reaches out_stream beside the norm.  dblock and dresidual may be
-    row inputs.  workspace: norm_gate_backward_workspace(block_out), allocated here when None."""
+    row inputs.  A row's products of two operands (dnormed, dstream or out_stream with block_out,
+    dnormed with out_stream, the squares of the last two) have to sum to float32 numbers.
+    workspace: norm_gate_backward_workspace(block_out), allocated here when None."""
     x = block_out
     rows, n, dt, dev = _train_rows(x, "block_out")
     if x.requires_grad:

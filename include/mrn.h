@@ -443,6 +443,12 @@ mrn_status mrn_norm_gate_backward_workspace(int64_t rows, int64_t n, int64_t *by
  *   dgate       = ds * gamma_post * xh  summed over the elements that share a gate
  *   dres_scale  = ds * residual         summed over the elements that share a scale
  * dblock and dresidual come from the f32 ds, each rounded once.
+ * Range: a row has six sums of products of its operands as they are, before inv scales
+ * them: out_stream^2, block_out^2 and, with cb = block_out * gamma_post (times a gate per
+ * channel), w * out_stream, w * cb, out_stream * cb and dstream * cb.  Where the magnitudes
+ * of one add up past f32's largest number, the row's gradients and those of the weights are
+ * unspecified (most often infinite or NaN), and products under f32's normal range (1e-38)
+ * lose bits: in both cases also where each gradient is an ordinary number.
  *   dnormed     [rows x n]  gradient of normed
  *   dstream     [rows x n]  or NULL: the gradient that reaches out_stream beside the norm
  *   residual    [rows x n]  the forward's; read only when dres_scale is asked for (else
@@ -478,8 +484,8 @@ mrn_status mrn_grad_norm_workspace(int64_t tensors, int64_t *bytes);
  *           type, MRN_F32 or MRN_BF16, mixed as they come
  *   norm    one f32 in device memory; 0 for an empty list
  * Sums over blocks of elements in f32, over the blocks in 64 bits, in a fixed order: the
- * same call gives the same bits.  Squares that leave f32's range are taken scaled, so that
- * norm is right wherever it is an f32 number itself; infinities give infinity, NaN gives
+ * same call gives the same bits.  Squares that leave f32's range are taken in 64 bits, so
+ * that norm is right wherever it is an f32 number itself; infinities give infinity, NaN gives
  * NaN.  A tensor that is listed twice counts twice.
  * Launches: one kernel per 960 tensors, and one.
  */
