@@ -558,7 +558,15 @@ struct GateBackwardLaunch {
 //         165, 154, 155, 156;  8192 166, 168, 162, 159;  12288 183, 152, 156, 140;  16384 175, 170, 188, 174
 //         a scale per channel: 2048 167, 168, 195, 163;  4096 160, 157, 160, 165;  6656, two CTAs a row,
 //         151 with one slot, 157, 163, 167
-// At 6656 f32 a row's four operands take 106 KB: two stages fit, and with two slots 13 warps.
+//   Around the band of two slots, f32, 4096 rows, with dstream, and without it:
+//         5600 121, 96, 94, 93;  6400 140, 107, 139, 140;  6655 162, 156, 155, 156;  6656 142, 114, 141, 141;
+//         6912 141, 149, 145, 144;  7168 143, 153, 152, 148;  7176 160, 182, 162, 164
+//         5600 108, 81, 78, 78;  6400 126, 91, 89, 89;  6655 145, 114, 99, 101;  6656 127, 94, 94, 93;
+//         6912 127, 99, 99, 99;  6911 148, 123, 101, 103;  7168 129, 105, 104, 103;  7176 141, 126, 112, 111
+// Up to 6656 f32 a row's four operands take 106 KB at most: two stages fit, and with two slots 13 warps
+// (with three, whose CTAs hold a multiple of 96 slots, the second stage misses by 1 KB).  Above, a CTA has
+// room for one, and up to 7168 all forms are within 8 %.  The rule does not look at dstream: without
+// it three slots would take 13 to 18 % less for rows with ends.
 template <class T> constexpr int gate_backward_slots(int64_t slots, bool edge, bool residual, bool columns) {
     if (T::kBytes == 2) {
         if (columns) return slots <= 384 ? 2 : 4;
@@ -580,10 +588,22 @@ template <class T> int gate_backward_threads(int64_t slots, int k, bool residual
     return threads > most ? most : threads;
 }
 
-// Whether any call takes this form: the forms that are compiled.  Rows that share a warp take all
-// of them, few rows one slot, and other rows of a CTA what the rule above gives for some width.
+// Whether rows of so few slots that they could share warps have CTAs of their own: f32 rows of more
+// slots than three for each lane of a warp, where four spill (32768 x 1024 167 us in warps, 142 in
+// CTAs of 128 threads; with ends 131 in warps).
+template <class T> constexpr bool gate_backward_apart(int64_t slots, bool edge) {
+    return T::kBytes == 4 && slots > 96 && !edge;
+}
+
+// Whether any call takes this form: the forms that are compiled.  Few rows take one slot, and rows
+// that share a warp and other rows of a CTA what the rules above give for some width.
 template <class T> constexpr bool gate_backward_chosen(int k, bool edge, bool warp, int res) {
-    if (warp || k == 1) return true;
+    if (k == 1) return true;
+    if (warp) {
+        for (int slots = 1; slots <= kWarpTileSlots; ++slots)
+            if (warp_tile_slots(slots) == k && !gate_backward_apart<T>(slots, edge)) return true;
+        return false;
+    }
     for (int slots = 1; slots <= kMaxCluster * kTileMaxThreads * 4; ++slots)
         if (gate_backward_slots<T>(slots, edge, res != 0, res == 2) == k) return true;
     return false;
@@ -660,10 +680,7 @@ cudaError_t launch_gate_backward_typed(const GateBackwardArgs &a, int sms, bool 
             const int k = few ? 1 : gate_backward_slots<T>(slots, edge, residual, columns);
             const int most_threads = few ? tile_few_threads(a.rows, a.n, sms)
                                          : gate_backward_threads<T>(slots, k, residual, columns);
-            // (f32 rows of more slots than three for each lane of a warp: four spill; 32768 x 1024 167 us in
-            // warps, 142 in CTAs of 128 threads)
-            const bool apart = T::kBytes == 4 && slots > 96 && !edge;
-            const TileShape p = tile_shape(a.n, mis, k, most_threads, few || apart);
+            const TileShape p = tile_shape(a.n, mis, k, most_threads, few || gate_backward_apart<T>(slots, edge));
             if (p.ok && p.warp) {
                 done = p.k == 1   ? launch_gate_backward_k<T, 1, true>(a, parts, p, l)
                        : p.k == 2 ? launch_gate_backward_k<T, 2, true>(a, parts, p, l)

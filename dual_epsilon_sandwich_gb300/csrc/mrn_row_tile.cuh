@@ -467,6 +467,10 @@ struct TileShape {
 
 constexpr int kWarpTileThreads = 128;
 constexpr int kWarpTileSlots = 128;    // rows of at most this many slots share warps
+// ... with so many slots per thread.
+constexpr int warp_tile_slots(int64_t slots) {
+    return slots <= 8 ? 1 : (slots <= 64 ? 2 : (slots <= 96 ? 3 : 4));
+}
 
 // Few rows, at most one per SM, of more slots than a warp's: what counts is how soon one row is
 // done.  One slot per thread, and a row of 512 slots or more over as many CTAs of 64
@@ -496,7 +500,7 @@ inline TileShape tile_shape(int64_t n, int mis, int k, int most_threads, bool fe
     const int64_t slots = n < 8 ? 1 : n / 8;
     if (slots <= kWarpTileSlots && !few) {
         s.warp = true;
-        s.k = slots <= 8 ? 1 : (slots <= 64 ? 2 : (slots <= 96 ? 3 : 4));
+        s.k = warp_tile_slots(slots);
         s.lanes = s.edge ? kEndLanes : 1;      // (a lane for each element at the ends)
         while (s.lanes * s.k < slots) s.lanes *= 2;
         s.threads = kWarpTileThreads;
