@@ -173,8 +173,8 @@ template <class T> constexpr int gate_backward_resident(int k, int res, bool war
 // mrn_row_tile.cuh); one reduction to a row, behind which the operands are read from the ring
 // once more.  RES: whether the residual is read for the gradient of its scale: 0 no, 1 a scalar,
 // 2 one value per channel, whose column sums are kept too.
-//   Measured on GB300, with the join: 16384 x 4096 bf16 with gate and scale learned per channel 169 us
-// (5.6 TB/s, 82 % of the copy's rate), without the scale 139 (5.8 TB/s); 16384 x 4095 bf16, a gate per row,
+//   Measured on GB300, with the join: 16384 x 4096 bf16 with gate and scale learned per channel 170 to 173
+// us (5.5 TB/s, 80 to 81 % of the copy's rate), without the scale 139 (5.8 TB/s); 16384 x 4095 bf16, a gate per row,
 // 148 (5.4 TB/s); 4096 x 6656 f32 without factors 110 to 114 (5.7 to 6.0 TB/s, where rmsnorm_backward twice
 // moves 8 matrices to its 6); 65536 x 768 bf16 103 (5.9 TB/s); 64 x 768 f32 5.0 us, two launches.
 //   What bounds it: warps.  The column sums and weights leave 8 to 16 of them on an SM, issuing in 26 to 57

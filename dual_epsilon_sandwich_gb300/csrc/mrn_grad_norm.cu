@@ -189,8 +189,8 @@ template <class T> __device__ __forceinline__ double slot_squares(const Slot<T> 
 
 constexpr int kListMixed = 2;      // slots of a thread in flight where a step meets several tensors
 
-// Memory bounds it: 0.58 G bf16 elements 165 us on the device (7.0 TB/s, 103 % of the copy's rate, whose
-// traffic is half writes), 128 bytes of each of 32 warps' threads in flight; 104 x 6656 f32 5.0 us
+// Memory bounds it: 0.58 G bf16 elements 171 to 176 us on the device (6.6 to 6.8 TB/s, 97 to 100 % of the
+// copy's rate, whose traffic is half writes), 128 bytes of each of 32 warps' threads in flight; 104 x 6656 f32 5.0 us
 // with the norm, two launches.
 template <int N>
 __global__ void __launch_bounds__(kListThreads, kListCtasPerSm)
@@ -309,7 +309,9 @@ __device__ __forceinline__ void list_store(Slot<F32> &s, const ListPlace &p, uin
 // what the squares read last may still be in L2.
 //   Memory bounds it: with the squares 0.58 G bf16 elements 540 to 550 us, 3.48 GB (6.3 TB/s, 94 %); 16.8 M
 // f32 elements 35 us, 5.7 TB/s.  Eviction hints (the stretch's end kept, the rest and the
-// outputs dropped first) gained 2 % at most and are not used.
+// outputs dropped first) gained 2 % at most and are not used.  In place takes the same where the limit is
+// reached, and little more than the norm where it is not (0.13 G bf16 elements 129 and 47 us); outputs at
+// other offsets than their inputs go element by element (403 us).
 template <int N>
 __global__ void __launch_bounds__(kListThreads, kListCtasPerSm)
 mrn_grad_scale_kernel(const __grid_constant__ ListArgs<N> l, const double *parts, int64_t count, double max_norm,
